@@ -57,6 +57,10 @@ typedef enum {
 } sp_status_t;
 
 typedef enum { SP_F32 = 0, SP_BF16 = 1 } sp_dtype_t;
+/* Element types of the 8-bit entry points: SP_F32 and SP_BF16 and the two
+ * 8-bit floating point formats, e4m3 (largest value 448, no infinities) and
+ * e5m2 (largest finite value 57344). */
+typedef enum { SP_ELEM_F32 = 0, SP_ELEM_BF16 = 1, SP_ELEM_E4M3 = 2, SP_ELEM_E5M2 = 3 } sp_elem_t;
 typedef enum { SP_RMSNORM = 0, SP_LAYERNORM = 1 } sp_norm_t;
 
 /* Problem statement of one SP region ([MT3] §3.2.1, §3.2.4; [SPN] LayerNorm
@@ -160,6 +164,121 @@ sp_status_t sp_rs_dropout_residual_norm_fwd_rows(const sp_rs_desc_t* desc,
                                                  uint8_t* mask_out,
                                                  float* rstd_out, float* mean_out,
                                                  sp_stream_t stream);
+
+/* 8-bit tensors.  An 8-bit tensor is a row-major matrix of e4m3 or e5m2 values
+ * with one scale per group of 128 consecutive values of a row (the last group
+ * of a row may be shorter); its value is q * 2^(byte - 127) where `byte` is
+ * the group's scale byte (the 8-bit exponent format ue8m0; 255 is NaN).
+ * The scale bytes of a tensor form a row-major matrix of ceil(columns/128)
+ * columns and either one row per row of the tensor or, for a tensor
+ * quantised in 128 x 128 blocks, one row per 128 rows.  Values and scales
+ * have row strides in bytes that are multiples of 16 and 16-byte aligned
+ * bases; what lies between the end of a row and its stride is neither read
+ * as a value nor written.
+ * Quantising a group: s is the smallest integer with max|x| <= 448 * 2^s
+ * (e4m3) or 57344 * 2^s (e5m2), at least -127; byte = s + 127 and
+ * q = x * 2^-s rounded to nearest even.  A group of zeros has s = 0.  A group
+ * that holds an infinity or a NaN gets byte 255 and NaN values. */
+
+/* The forward of the SP region with the norm's output in 8 bits, for a
+ * column-parallel product in 8 bits behind it (and a half as large
+ * all-gather in front of that): sp_rs_dropout_residual_norm_fwd with y
+ * quantised to e4m3, one scale per token and 128 columns, straight from its
+ * fp32 value.  With T = 1 and p = 0 it is the residual's addition and the norm.
+ * Everything else (h_out, mask_out, rstd_out, mean_out) is as in that call,
+ * bit for bit, so sp_rs_dropout_residual_norm_bwd is its backward too (y's
+ * rounding is passed straight through, as that of a 16-bit y is).
+ *
+ * q_out: [nshards*R, H] e4m3, ldq bytes between rows; scale_out: [nshards*R,
+ * ceil(H/128)] scale bytes, ldscale bytes between rows.
+ * Errors: as that call; besides, SP_ERR_SHAPE for a stride that is too short
+ * or no multiple of 16, SP_ERR_ALIGN for q_out or scale_out. */
+sp_status_t sp_rs_dropout_residual_norm_fwd_q8(const sp_rs_desc_t* desc,
+                                               const void* const* partials,
+                                               const void* residual,
+                                               const void* gamma, const void* beta,
+                                               void* h_out, uint8_t* q_out, int64_t ldq,
+                                               uint8_t* scale_out, int64_t ldscale,
+                                               uint8_t* mask_out,
+                                               float* rstd_out, float* mean_out,
+                                               sp_stream_t stream);
+
+/* The same restricted to rows [row_begin, row_begin + row_count), as
+ * sp_rs_dropout_residual_norm_fwd_rows: q_out and scale_out address the
+ * call's row 0 as well. */
+sp_status_t sp_rs_dropout_residual_norm_fwd_q8_rows(const sp_rs_desc_t* desc,
+                                                    int64_t row_begin, int64_t row_count,
+                                                    const void* const* partials,
+                                                    const void* residual, const void* gamma,
+                                                    const void* beta, void* h_out,
+                                                    uint8_t* q_out, int64_t ldq,
+                                                    uint8_t* scale_out, int64_t ldscale,
+                                                    uint8_t* mask_out,
+                                                    float* rstd_out, float* mean_out,
+                                                    sp_stream_t stream);
+
+/* Quantises x [M, K] to 8 bits: along its rows (q [M, K]: the operand whose
+ * contraction runs over K), along its columns (qt [K, M], the transposed
+ * tensor: the operand whose contraction runs over M), or both in one pass.
+ * With block != 0 the groups are 128 x 128 blocks, and qt holds q's values
+ * transposed.  x may be an 8-bit tensor itself: it is read as the values it
+ * stands for (a saved 8-bit activation, requantised along its tokens). */
+typedef struct sp_quantize_q8_desc_t {
+  int64_t M, K;         /* both below 2^31 */
+  int64_t ldx;          /* elements between rows of x */
+  int64_t ldx_scale;    /* 8-bit x: bytes between rows of x_scale */
+  int64_t ldq;          /* bytes between rows of q, of its scales, */
+  int64_t ldq_scale;
+  int64_t ldqt;         /* of qt and of its scales */
+  int64_t ldqt_scale;
+  int32_t x_dtype;      /* sp_elem_t */
+  int32_t q_dtype;      /* SP_ELEM_E4M3 or SP_ELEM_E5M2 */
+  int32_t x_scale_rows; /* 8-bit x: rows that share a scale, 1 or 128 */
+  int32_t block;        /* 0: groups of 128 values, 1: blocks of 128 x 128 */
+  int64_t reserved;     /* must be 0 */
+} sp_quantize_q8_desc_t;
+
+/* x: element-aligned (any row stride of at least K); an 8-bit x as any 8-bit
+ * tensor.  x_scale: an 8-bit x's scales, else ignored.  q and q_scale, or qt
+ * and qt_scale, may be NULL: that output is then not made (their strides are
+ * ignored).  Scales: q_scale has M rows (ceil(M/128) with block), qt_scale
+ * has K rows (ceil(K/128)).
+ * Errors: SP_ERR_DTYPE, SP_ERR_SHAPE (sizes, strides), SP_ERR_INVALID_ARG
+ * (NULL pointers, no output at all, x_scale_rows, block, reserved),
+ * SP_ERR_ALIGN, SP_ERR_CUDA.  M == 0 or K == 0 returns SP_OK at once. */
+sp_status_t sp_quantize_q8(const sp_quantize_q8_desc_t* desc, const void* x,
+                           const uint8_t* x_scale, uint8_t* q, uint8_t* q_scale,
+                           uint8_t* qt, uint8_t* qt_scale, sp_stream_t stream);
+
+/* C = A B^T (or C += A B^T) of 8-bit tensors A [M, K] and B [N, K]:
+ *   C[i,j] = sum_k A[i,k] B[j,k],  A and B the values the tensors stand for,
+ * sums in fp32, one rounding to C's type.  The three products of a linear
+ * layer y = x W^T: y from x and W; dx from dy and W^T; dW from dy^T and x^T
+ * (the transposed tensors as sp_quantize_q8 makes them). */
+typedef struct sp_matmul_q8_desc_t {
+  int64_t M, N, K;        /* each below 2^31 */
+  int64_t lda, ldb;       /* bytes between rows of A and of B */
+  int64_t lda_scale;      /* bytes between rows of their scales */
+  int64_t ldb_scale;
+  int64_t ldc;            /* elements between rows of C, at least N */
+  int32_t a_dtype;        /* SP_ELEM_E4M3 or SP_ELEM_E5M2, each */
+  int32_t b_dtype;
+  int32_t c_dtype;        /* SP_ELEM_F32 or SP_ELEM_BF16 */
+  int32_t a_scale_rows;   /* rows that share a scale: 1, or 128 (blocks) */
+  int32_t b_scale_rows;
+  int32_t accumulate;     /* 1: add to what C holds (SP_ELEM_F32 only) */
+  uint32_t* status;       /* as in sp_rs_desc_t */
+} sp_matmul_q8_desc_t;
+
+/* c: element-aligned, must not overlap A, B or the scales; only its M x N
+ * elements are written.  K == 0 writes zeros (or leaves C when accumulating);
+ * A, B and the scales may then be NULL.  M == 0 or N == 0 returns SP_OK at
+ * once.  Errors: SP_ERR_DTYPE (types; accumulating in bf16), SP_ERR_SHAPE
+ * (sizes, strides), SP_ERR_INVALID_ARG (NULL pointers, scale_rows,
+ * accumulate), SP_ERR_ALIGN, SP_ERR_CUDA. */
+sp_status_t sp_matmul_q8(const sp_matmul_q8_desc_t* desc, const uint8_t* a,
+                         const uint8_t* a_scale, const uint8_t* b,
+                         const uint8_t* b_scale, void* c, sp_stream_t stream);
 
 /* Bytes of device workspace sp_rs_dropout_residual_norm_bwd needs for this
  * problem on the CURRENT device (it depends on the SM count).  Returns 0 for

@@ -10,10 +10,12 @@
 
 #include "../../include/spfuse.h"
 #include "launch.h"
+#include "q8.cuh"
 
 namespace spf {
 namespace {
 
+constexpr int64_t kMaxQ8Dim = (int64_t)1 << 31;  // each side of an 8-bit tensor stays below this
 constexpr int kMaxFwdTPR = 512;
 constexpr int kMaxVPT = 4;
 
@@ -182,13 +184,34 @@ sp_status_t plan_bwd(const Problem& pr, bool has_dh, bool has_mask, BwdPlan* pl)
   return SP_OK;
 }
 
+// Where the forward's 8-bit y goes; q == nullptr in a call with y in the
+// activation type.
+struct Q8Out {
+  bool on;
+  uint8_t* q;
+  int64_t ldq;
+  uint8_t* scale;
+  int64_t ldscale;
+};
+
+int64_t q8_groups(int64_t n) { return (n + kQ8Group - 1) / kQ8Group; }
+
+// Row strides of an 8-bit tensor of `rows` rows of `cols` values and of its
+// scales (srows rows of them): both multiples of 16 bytes, long enough, and
+// the last row's offset well inside 64 bits.
+bool q8_strides_ok(int64_t rows, int64_t cols, int64_t ld, int64_t srows, int64_t ldscale) {
+  const int64_t most = (int64_t)1 << 61;
+  return ld >= cols && ld % 16 == 0 && ldscale >= q8_groups(cols) && ldscale % 16 == 0 &&
+         (rows == 0 || ld <= most / rows) && (srows == 0 || ldscale <= most / srows);
+}
+
 // The forward over rows [row_begin, row_begin + row_count) of the call's
 // nshards*R rows (all of them unless `ranged`).  Per-row arguments address
 // the call's row 0; the partials and the dropout mask follow the global row
 // index, so a range computes exactly what the full call computes there.
 sp_status_t fwd_impl(const sp_rs_desc_t* desc, bool ranged, int64_t row_begin, int64_t row_count,
                      const void* const* partials, const void* residual, const void* gamma,
-                     const void* beta, void* h_out, void* y_out, uint8_t* mask_out,
+                     const void* beta, void* h_out, void* y_out, const Q8Out& q8, uint8_t* mask_out,
                      float* rstd_out, float* mean_out, sp_stream_t stream) {
   Problem pr;
   sp_status_t st = check_desc(desc, &pr);
@@ -200,8 +223,10 @@ sp_status_t fwd_impl(const sp_rs_desc_t* desc, bool ranged, int64_t row_begin, i
   } else if (row_begin < 0 || row_count < 0 || row_begin > pr.rows || row_count > pr.rows - row_begin) {
     return SP_ERR_INVALID_ARG;
   }
+  if (q8.on && !q8_strides_ok(pr.rows, pr.H, q8.ldq, pr.rows, q8.ldscale)) return SP_ERR_SHAPE;
   if (row_count == 0) return SP_OK;  // nothing to read or write
-  if (!partials || !residual || !gamma || !h_out || !y_out || !rstd_out) return SP_ERR_INVALID_ARG;
+  if (!partials || !residual || !gamma || !h_out || !rstd_out) return SP_ERR_INVALID_ARG;
+  if (q8.on ? !q8.q || !q8.scale : !y_out) return SP_ERR_INVALID_ARG;
   if (ln && (!beta || !mean_out)) return SP_ERR_INVALID_ARG;
   for (int t = 0; t < pr.T; ++t) {
     if (!partials[t]) return SP_ERR_INVALID_ARG;
@@ -211,11 +236,18 @@ sp_status_t fwd_impl(const sp_rs_desc_t* desc, bool ranged, int64_t row_begin, i
   const int64_t rowb = pr.H * elem_bytes(pr.dtype);
   residual = static_cast<const char*>(residual) + row_begin * rowb;
   h_out = static_cast<char*>(h_out) + row_begin * rowb;
-  y_out = static_cast<char*>(y_out) + row_begin * rowb;
+  uint8_t* yscale = nullptr;
+  if (q8.on) {
+    y_out = q8.q + row_begin * q8.ldq;
+    yscale = q8.scale + row_begin * q8.ldscale;
+  } else {
+    y_out = static_cast<char*>(y_out) + row_begin * rowb;
+  }
   if (mask_out) mask_out += row_begin * pr.H;
   rstd_out += row_begin;
   if (ln) mean_out += row_begin;
   if (!aligned(residual, 16) || !aligned(gamma, 16) || !aligned(h_out, 16) || !aligned(y_out, 16) ||
+      !aligned(yscale, 16) ||
       (ln && !aligned(beta, 16)) || (mask_out && !aligned(mask_out, 16)) || !aligned(rstd_out, 4) ||
       (ln && !aligned(mean_out, 4)))
     return SP_ERR_ALIGN;
@@ -227,6 +259,9 @@ sp_status_t fwd_impl(const sp_rs_desc_t* desc, bool ranged, int64_t row_begin, i
   a.beta = ln ? beta : nullptr;
   a.h = h_out;
   a.y = y_out;
+  a.yscale = yscale;
+  a.ldq = q8.ldq;
+  a.ldscale = q8.ldscale;
   a.mask = mask_out;
   a.rstd = rstd_out;
   a.mean = ln ? mean_out : nullptr;
@@ -264,6 +299,9 @@ sp_status_t fwd_impl(const sp_rs_desc_t* desc, bool ranged, int64_t row_begin, i
     if (plan_fwd_tma(pr.H, pr.T, ln, optin, row_count, sms, &tp)) {
       a.tpr = tp.shape.tpr;
       const dim3 grid((unsigned)((row_count + tp.layout.rows_per_cta - 1) / tp.layout.rows_per_cta));
+      if (q8.on)
+        return from_cuda(ln ? launch_fwd_tma_ln_q8(a, pr.T, tp, grid, cs)
+                            : launch_fwd_tma_rms_q8(a, pr.T, tp, grid, cs));
       return from_cuda(ln ? launch_fwd_tma_ln(a, pr.T, tp, grid, cs)
                           : launch_fwd_tma_rms(a, pr.T, tp, grid, cs));
     }
@@ -273,7 +311,11 @@ sp_status_t fwd_impl(const sp_rs_desc_t* desc, bool ranged, int64_t row_begin, i
   const int rpc = s.block / s.tpr;
   const dim3 grid((unsigned)((row_count + rpc - 1) / rpc));
   cudaError_t e;
-  if (pr.dtype == SP_BF16)
+  if (q8.on && pr.dtype == SP_BF16)
+    e = ln ? launch_fwd_bf16_ln_q8(a, pr.T, s, grid, cs) : launch_fwd_bf16_rms_q8(a, pr.T, s, grid, cs);
+  else if (q8.on)
+    e = ln ? launch_fwd_f32_ln_q8(a, pr.T, s, grid, cs) : launch_fwd_f32_rms_q8(a, pr.T, s, grid, cs);
+  else if (pr.dtype == SP_BF16)
     e = ln ? launch_fwd_bf16_ln(a, pr.T, s, grid, cs) : launch_fwd_bf16_rms(a, pr.T, s, grid, cs);
   else
     e = ln ? launch_fwd_f32_ln(a, pr.T, s, grid, cs) : launch_fwd_f32_rms(a, pr.T, s, grid, cs);
@@ -392,8 +434,8 @@ sp_status_t sp_rs_dropout_residual_norm_fwd(const sp_rs_desc_t* desc, const void
                                             const void* beta, void* h_out, void* y_out,
                                             uint8_t* mask_out, float* rstd_out, float* mean_out,
                                             sp_stream_t stream) {
-  return fwd_impl(desc, false, 0, 0, partials, residual, gamma, beta, h_out, y_out, mask_out, rstd_out,
-                  mean_out, stream);
+  return fwd_impl(desc, false, 0, 0, partials, residual, gamma, beta, h_out, y_out, Q8Out{}, mask_out,
+                  rstd_out, mean_out, stream);
 }
 
 sp_status_t sp_rs_dropout_residual_norm_fwd_rows(const sp_rs_desc_t* desc, int64_t row_begin,
@@ -403,7 +445,122 @@ sp_status_t sp_rs_dropout_residual_norm_fwd_rows(const sp_rs_desc_t* desc, int64
                                                  uint8_t* mask_out, float* rstd_out, float* mean_out,
                                                  sp_stream_t stream) {
   return fwd_impl(desc, true, row_begin, row_count, partials, residual, gamma, beta, h_out, y_out,
-                  mask_out, rstd_out, mean_out, stream);
+                  Q8Out{}, mask_out, rstd_out, mean_out, stream);
+}
+
+sp_status_t sp_rs_dropout_residual_norm_fwd_q8(const sp_rs_desc_t* desc, const void* const* partials,
+                                               const void* residual, const void* gamma,
+                                               const void* beta, void* h_out, uint8_t* q_out,
+                                               int64_t ldq, uint8_t* scale_out, int64_t ldscale,
+                                               uint8_t* mask_out, float* rstd_out, float* mean_out,
+                                               sp_stream_t stream) {
+  return fwd_impl(desc, false, 0, 0, partials, residual, gamma, beta, h_out, nullptr,
+                  Q8Out{true, q_out, ldq, scale_out, ldscale}, mask_out, rstd_out, mean_out, stream);
+}
+
+sp_status_t sp_rs_dropout_residual_norm_fwd_q8_rows(const sp_rs_desc_t* desc, int64_t row_begin,
+                                                    int64_t row_count, const void* const* partials,
+                                                    const void* residual, const void* gamma,
+                                                    const void* beta, void* h_out, uint8_t* q_out,
+                                                    int64_t ldq, uint8_t* scale_out, int64_t ldscale,
+                                                    uint8_t* mask_out, float* rstd_out,
+                                                    float* mean_out, sp_stream_t stream) {
+  return fwd_impl(desc, true, row_begin, row_count, partials, residual, gamma, beta, h_out, nullptr,
+                  Q8Out{true, q_out, ldq, scale_out, ldscale}, mask_out, rstd_out, mean_out, stream);
+}
+
+sp_status_t sp_quantize_q8(const sp_quantize_q8_desc_t* d, const void* x, const uint8_t* x_scale,
+                           uint8_t* q, uint8_t* q_scale, uint8_t* qt, uint8_t* qt_scale,
+                           sp_stream_t stream) {
+  if (!d) return SP_ERR_INVALID_ARG;
+  const bool x8 = d->x_dtype == SP_ELEM_E4M3 || d->x_dtype == SP_ELEM_E5M2;
+  if (!x8 && d->x_dtype != SP_ELEM_F32 && d->x_dtype != SP_ELEM_BF16) return SP_ERR_DTYPE;
+  if (d->q_dtype != SP_ELEM_E4M3 && d->q_dtype != SP_ELEM_E5M2) return SP_ERR_DTYPE;
+  if (d->reserved != 0 || (d->block != 0 && d->block != 1) ||
+      (x8 && d->x_scale_rows != 1 && d->x_scale_rows != kQ8Group))
+    return SP_ERR_INVALID_ARG;
+  if (d->M < 0 || d->K < 0 || d->M >= kMaxQ8Dim || d->K >= kMaxQ8Dim) return SP_ERR_SHAPE;
+  const int64_t mg = q8_groups(d->M), kg = q8_groups(d->K);
+  if (mg > 0 && kg > (((int64_t)1 << 31) - 1) / mg) return SP_ERR_SHAPE;  // 128 x 128 tiles in the grid
+  if (d->ldx < d->K || (d->M > 0 && d->ldx > ((int64_t)1 << 58) / d->M)) return SP_ERR_SHAPE;
+  if (x8 && !q8_strides_ok(d->M, d->K, d->ldx, d->M, d->ldx_scale)) return SP_ERR_SHAPE;
+  if (!q && !qt) return SP_ERR_INVALID_ARG;
+  if (q && !q8_strides_ok(d->M, d->K, d->ldq, d->block ? mg : d->M, d->ldq_scale)) return SP_ERR_SHAPE;
+  if (qt && !q8_strides_ok(d->K, d->M, d->ldqt, d->block ? kg : d->K, d->ldqt_scale)) return SP_ERR_SHAPE;
+  if (d->M == 0 || d->K == 0) return SP_OK;  // nothing to read or write
+  if (!x || (x8 && !x_scale) || (q && !q_scale) || (qt && !qt_scale)) return SP_ERR_INVALID_ARG;
+  const int xb = x8 ? 1 : d->x_dtype == SP_ELEM_BF16 ? 2 : 4;
+  if (!aligned(x, x8 ? 16 : xb) || (x8 && !aligned(x_scale, 16)) || !aligned(q, 16) || !aligned(q_scale, 16) ||
+      !aligned(qt, 16) || !aligned(qt_scale, 16))
+    return SP_ERR_ALIGN;
+  QuantArgs a = {};
+  a.x = x;
+  a.x_scale = x_scale;
+  a.q = q;
+  a.q_scale = q_scale;
+  a.qt = qt;
+  a.qt_scale = qt_scale;
+  a.M = d->M;
+  a.K = d->K;
+  a.ldx = d->ldx;
+  a.ldq = d->ldq;
+  a.ldqt = d->ldqt;
+  a.ldx_scale = d->ldx_scale;
+  a.ldq_scale = d->ldq_scale;
+  a.ldqt_scale = d->ldqt_scale;
+  a.ktiles = kg;
+  a.x_scale_rows = d->x_scale_rows;
+  a.x_e5m2 = d->x_dtype == SP_ELEM_E5M2;
+  a.vec = aligned(x, 16) && d->ldx * xb % 16 == 0;
+  if (inject_launch_failure()) return SP_ERR_CUDA;
+  return from_cuda(launch_quant_q8(a, d->x_dtype, d->q_dtype == SP_ELEM_E5M2, d->block != 0,
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+sp_status_t sp_matmul_q8(const sp_matmul_q8_desc_t* d, const uint8_t* a, const uint8_t* a_scale,
+                         const uint8_t* b, const uint8_t* b_scale, void* c, sp_stream_t stream) {
+  if (!d) return SP_ERR_INVALID_ARG;
+  for (const int32_t t : {d->a_dtype, d->b_dtype})
+    if (t != SP_ELEM_E4M3 && t != SP_ELEM_E5M2) return SP_ERR_DTYPE;
+  if (d->c_dtype != SP_ELEM_F32 && d->c_dtype != SP_ELEM_BF16) return SP_ERR_DTYPE;
+  for (const int32_t r : {d->a_scale_rows, d->b_scale_rows})
+    if (r != 1 && r != kQ8Group) return SP_ERR_INVALID_ARG;
+  if (d->accumulate != 0 && d->accumulate != 1) return SP_ERR_INVALID_ARG;
+  if (d->accumulate && d->c_dtype != SP_ELEM_F32) return SP_ERR_DTYPE;  // sums are kept in fp32
+  if (!aligned(d->status, 4)) return SP_ERR_ALIGN;
+  if (d->M < 0 || d->N < 0 || d->K < 0 || d->M >= kMaxQ8Dim || d->N >= kMaxQ8Dim || d->K >= kMaxQ8Dim)
+    return SP_ERR_SHAPE;
+  const int64_t am = d->a_scale_rows == 1 ? d->M : q8_groups(d->M), bn = d->b_scale_rows == 1 ? d->N : q8_groups(d->N);
+  if (!q8_strides_ok(d->M, d->K, d->lda, am, d->lda_scale) || !q8_strides_ok(d->N, d->K, d->ldb, bn, d->ldb_scale))
+    return SP_ERR_SHAPE;
+  if (d->ldc < d->N || (d->M > 0 && d->ldc > ((int64_t)1 << 58) / d->M)) return SP_ERR_SHAPE;
+  if (d->M == 0 || d->N == 0) return SP_OK;  // nothing to write
+  if (!c || (d->K > 0 && (!a || !a_scale || !b || !b_scale))) return SP_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(a_scale, 16) || !aligned(b, 16) || !aligned(b_scale, 16) ||
+      !aligned(c, d->c_dtype == SP_ELEM_F32 ? 4 : 2))
+    return SP_ERR_ALIGN;
+  MatmulArgs m = {};
+  m.a = a;
+  m.a_scale = a_scale;
+  m.b = b;
+  m.b_scale = b_scale;
+  m.c = c;
+  m.M = d->M;
+  m.N = d->N;
+  m.K = d->K;
+  m.lda = d->lda;
+  m.ldb = d->ldb;
+  m.ldc = d->ldc;
+  m.lda_scale = d->lda_scale;
+  m.ldb_scale = d->ldb_scale;
+  m.a_scale_rows = d->a_scale_rows;
+  m.b_scale_rows = d->b_scale_rows;
+  m.a_e5m2 = d->a_dtype == SP_ELEM_E5M2;
+  m.b_e5m2 = d->b_dtype == SP_ELEM_E5M2;
+  m.c_f32 = d->c_dtype == SP_ELEM_F32;
+  m.accumulate = d->accumulate;
+  if (inject_launch_failure()) return SP_ERR_CUDA;
+  return from_cuda(launch_matmul_q8(m, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t sp_rs_bwd_workspace_bytes(const sp_rs_desc_t* desc) {

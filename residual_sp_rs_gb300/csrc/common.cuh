@@ -388,10 +388,13 @@ struct FwdArgs {
   const void* gamma;     // [H]
   const void* beta;      // [H] (LayerNorm)
   void* h;               // [rows, H]
-  void* y;               // [rows, H]
+  void* y;               // [rows, H]; the 8-bit instances: [rows, ldq] bytes
   uint8_t* mask;         // [rows, H] or null
   float* rstd;           // [rows]
   float* mean;           // [rows] (LayerNorm)
+  uint8_t* yscale;       // 8-bit instances: [rows, ldscale] scale bytes of y
+  int64_t ldq;           // 8-bit instances: bytes between rows of y
+  int64_t ldscale;       // 8-bit instances: bytes between rows of yscale
   int64_t rows;          // token rows processed
   int64_t grow0;         // global row index of local row 0 (j * R)
   int32_t H;
@@ -437,6 +440,37 @@ struct BwdArgs {
   uint32_t* status;      // device status word (timeouts are ORed in) or null
   uint64_t wait_ns;      // bound of every mbarrier wait
   int32_t drop_stage;    // test hook: CTA 0's producer never fills this stage (-1: none)
+};
+
+struct QuantArgs {
+  const void* x;            // [M, K]
+  const uint8_t* x_scale;   // scale bytes of an 8-bit x
+  uint8_t* q;               // [M, K] or null
+  uint8_t* q_scale;
+  uint8_t* qt;              // [K, M] or null
+  uint8_t* qt_scale;
+  int64_t M, K;
+  int64_t ldx, ldq, ldqt;                      // elements between rows
+  int64_t ldx_scale, ldq_scale, ldqt_scale;    // bytes between rows of scales
+  int64_t ktiles;           // 128-column tiles
+  int32_t x_scale_rows;     // rows that share a scale of x: 1 or 128
+  int32_t x_e5m2;
+  int32_t vec;              // x allows aligned vector loads
+};
+
+struct MatmulArgs {
+  const uint8_t* a;         // [M, K]
+  const uint8_t* a_scale;
+  const uint8_t* b;         // [N, K]
+  const uint8_t* b_scale;
+  void* c;                  // [M, N]
+  int64_t M, N, K;
+  int64_t lda, ldb, ldc;               // elements between rows
+  int64_t lda_scale, ldb_scale;        // bytes between rows of scales
+  int32_t a_scale_rows, b_scale_rows;  // rows that share a scale: 1 or 128
+  int32_t a_e5m2, b_e5m2;
+  int32_t c_f32;
+  int32_t accumulate;
 };
 
 // Bits of the device status word (the values of include/spfuse.h).

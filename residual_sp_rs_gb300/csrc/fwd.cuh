@@ -7,14 +7,16 @@
 // them is used, so each thread keeps (T+1)*VPT*16 bytes in flight; gamma and
 // beta are staged once per CTA in shared memory meanwhile.  The stored
 // (rounded) residual stream stays in registers, packed, for the norm: HBM is
-// read once per input and written once per output.
+// read once per input and written once per output.  Q8: y leaves in e4m3 with
+// a scale byte per 128 columns (128/EV neighbouring lanes of a row).
 #pragma once
 
 #include "common.cuh"
+#include "q8.cuh"
 
 namespace spf {
 
-template <typename Act, int T, bool LN, int VPT>
+template <typename Act, int T, bool LN, int VPT, bool Q8>
 __global__ void __launch_bounds__(512) sp_fwd_kernel(const FwdArgs a) {
   using V = Act16<Act>;
   constexpr int EV = V::EV;
@@ -167,7 +169,35 @@ __global__ void __launch_bounds__(512) sp_fwd_kernel(const FwdArgs a) {
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int v = lr + k * tpr;
-    if (v < a.nvec) {
+    if constexpr (Q8) {
+      float yv[EV] = {};
+      uint32_t amax = 0u;
+      if (v < a.nvec) {
+        float gm[EV], hr[EV], bt[EV];
+        V::unpack(sgb[v], gm);
+        if constexpr (LN) V::unpack(sgb[a.nvec + v], bt);
+        if constexpr (EV == 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f2_split(hf[k][i], hr[2 * i], hr[2 * i + 1]);
+        } else {
+          V::unpack(hp[k], hr);
+        }
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
+          yv[e] = LN ? gm[e] * ((hr[e] - mu) * rstd) + bt[e] : gm[e] * (hr[e] * rstd);
+          amax = max(amax, abs_bits(yv[e]));
+        }
+      }
+      const uint32_t sb = q8_scale_byte<false>(lanes_max<kQ8Group / EV>(amax));  // every lane takes part
+      if (v < a.nvec) {
+        const float inv = q8_inv_scale(sb);
+        uint32_t* yq = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.y) + r * a.ldq + (int64_t)v * EV);
+#pragma unroll
+        for (int e = 0; e < EV; e += 4)
+          yq[e / 4] = q8_pack4<false>(yv[e] * inv, yv[e + 1] * inv, yv[e + 2] * inv, yv[e + 3] * inv);
+        if ((v & (kQ8Group / EV - 1)) == 0) a.yscale[r * a.ldscale + v / (kQ8Group / EV)] = (uint8_t)sb;
+      }
+    } else if (v < a.nvec) {
       uint4 yout;
       if constexpr (EV == 8) {
         const f2_t r2 = f2(rstd, rstd), mu2 = f2(mu, mu);

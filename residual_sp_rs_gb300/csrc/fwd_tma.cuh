@@ -24,11 +24,17 @@
 // input) -- so a row is VPT stages, each released as soon as its slot's h is
 // in registers.
 //
+// Q8: y leaves in e4m3 with a scale byte per 128 columns instead of bf16.  A
+// group is 16 neighbouring lanes' vectors (its maximum is four shuffles); the
+// fp32 value of y is scaled and rounded to 8 bits at once, without the
+// rounding to bf16 in between.
+//
 // If a wait times out, the row group stops, writes NaN into the rstd of the
 // rows it did not finish and reports the timeout in the device status word.
 #pragma once
 
 #include "common.cuh"
+#include "q8.cuh"
 #include "tma.cuh"
 
 namespace spf {
@@ -121,7 +127,7 @@ struct HRow {
 // FAST: p > 0 with 1/(1-p) not dyadic (the common case) -- no tie rule, no
 // runtime mode branches in the element loop.  Otherwise GENERIC.
 
-template <int T, bool LN, int VPT, bool FAST, int NTHR, bool CH>
+template <int T, bool LN, int VPT, bool FAST, int NTHR, bool CH, bool Q8>
 __global__ void __launch_bounds__(NTHR, 1) sp_fwd_tma_kernel(const FwdArgs a, const FwdTmaLayout L) {
   constexpr int EV = 8;
   constexpr int NCH = CH ? VPT : 1;  // stages per row stage (CH: rb == 1)
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(NTHR, 1) sp_fwd_tma_kernel(const FwdArgs a, co
     const unsigned char* st = stages + (size_t)s * L.stage_bytes + (size_t)ri * rowb;
     int cs = s, cpar = par;  // CH: the ring slot of column chunk k
     __nv_bfloat16* h_row = reinterpret_cast<__nv_bfloat16*>(a.h) + r * (int64_t)H;
-    __nv_bfloat16* y_row = reinterpret_cast<__nv_bfloat16*>(a.y) + r * (int64_t)H;
+    __nv_bfloat16* y_row = Q8 ? nullptr : reinterpret_cast<__nv_bfloat16*>(a.y) + r * (int64_t)H;
 
     // ---- reduce, dropout, residual add; store h ----------------------------
     // h stays in registers for the norm, as fp32 pairs
@@ -424,7 +430,43 @@ __global__ void __launch_bounds__(NTHR, 1) sp_fwd_tma_kernel(const FwdArgs a, co
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = lr + k * tpr;
-      if (k < VPT - 1 || last_in) {
+      if constexpr (Q8) {
+        f2_t yv[4] = {};
+        uint32_t amax = 0u;
+        if (k < VPT - 1 || last_in) {
+          const float4* gp = reinterpret_cast<const float4*>(sgb) + v;
+#pragma unroll
+          for (int q2 = 0; q2 < 2; ++q2) {
+            const float4 g4 = gp[q2 * nvec];
+            const f2_t ga = f2(g4.x, g4.y), gb = f2(g4.z, g4.w);
+            if constexpr (LN) {
+              const float4 b4 = (reinterpret_cast<const float4*>(sgb + H) + v)[q2 * nvec];
+              yv[2 * q2] = f2_fma(ga, f2_mul(f2_sub(hf.get(k, 2 * q2), mu2), r2), f2(b4.x, b4.y));
+              yv[2 * q2 + 1] = f2_fma(gb, f2_mul(f2_sub(hf.get(k, 2 * q2 + 1), mu2), r2), f2(b4.z, b4.w));
+            } else {
+              yv[2 * q2] = f2_mul(ga, f2_mul(hf.get(k, 2 * q2), r2));
+              yv[2 * q2 + 1] = f2_mul(gb, f2_mul(hf.get(k, 2 * q2 + 1), r2));
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float lo, hi;
+            f2_split(yv[q], lo, hi);
+            amax = max(amax, max(abs_bits(lo), abs_bits(hi)));
+          }
+        }
+        const uint32_t sb = q8_scale_byte<false>(lanes_max<16>(amax));  // every lane takes part
+        if (k < VPT - 1 || last_in) {
+          const float inv = q8_inv_scale(sb);
+          const f2_t inv2 = f2(inv, inv);
+          float e[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) f2_split(f2_mul(yv[q], inv2), e[2 * q], e[2 * q + 1]);
+          *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.y) + r * a.ldq + (int64_t)v * EV) =
+              make_uint2(q8_pack4<false>(e[0], e[1], e[2], e[3]), q8_pack4<false>(e[4], e[5], e[6], e[7]));
+          if ((v & 15) == 0) a.yscale[r * a.ldscale + (v >> 4)] = (uint8_t)sb;
+        }
+      } else if (k < VPT - 1 || last_in) {
         const float4* gp = reinterpret_cast<const float4*>(sgb) + v;
         uint32_t yw[4];
 #pragma unroll

@@ -4,6 +4,6 @@
 namespace spf {
 cudaError_t launch_fwd_tma_ln_ch(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid,
                                    cudaStream_t st) {
-  return launch_fwd_tma_impl<true, true>(a, T, p, grid, st);
+  return launch_fwd_tma_impl<true, true, false>(a, T, p, grid, st);
 }
 }  // namespace spf

@@ -1,0 +1,10 @@
+// TMA-fed forward instances with y in 8 bits: bf16, norm ln, whole-row stages.
+#include "fwd_tma_inst.cuh"
+
+namespace spf {
+cudaError_t launch_fwd_tma_ln_q8(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid,
+                                  cudaStream_t st) {
+  if (p.chunked) return launch_fwd_tma_ln_ch_q8(a, T, p, grid, st);
+  return launch_fwd_tma_impl<true, false, true>(a, T, p, grid, st);
+}
+}  // namespace spf

@@ -5,6 +5,6 @@ namespace spf {
 cudaError_t launch_fwd_tma_rms(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid,
                                 cudaStream_t st) {
   if (p.chunked) return launch_fwd_tma_rms_ch(a, T, p, grid, st);
-  return launch_fwd_tma_impl<false, false>(a, T, p, grid, st);
+  return launch_fwd_tma_impl<false, false, false>(a, T, p, grid, st);
 }
 }  // namespace spf

@@ -108,6 +108,20 @@ cudaError_t launch_fwd_tma_ln(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3
 cudaError_t launch_fwd_tma_rms_ch(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid, cudaStream_t st);
 cudaError_t launch_fwd_tma_ln_ch(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid, cudaStream_t st);
 
+// The same with y in 8 bits.
+cudaError_t launch_fwd_bf16_rms_q8(const FwdArgs& a, int T, const RowShape& s, dim3 grid, cudaStream_t st);
+cudaError_t launch_fwd_bf16_ln_q8(const FwdArgs& a, int T, const RowShape& s, dim3 grid, cudaStream_t st);
+cudaError_t launch_fwd_f32_rms_q8(const FwdArgs& a, int T, const RowShape& s, dim3 grid, cudaStream_t st);
+cudaError_t launch_fwd_f32_ln_q8(const FwdArgs& a, int T, const RowShape& s, dim3 grid, cudaStream_t st);
+cudaError_t launch_fwd_tma_rms_q8(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid, cudaStream_t st);
+cudaError_t launch_fwd_tma_ln_q8(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid, cudaStream_t st);
+cudaError_t launch_fwd_tma_rms_ch_q8(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid, cudaStream_t st);
+cudaError_t launch_fwd_tma_ln_ch_q8(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid, cudaStream_t st);
+
+// x_dtype: sp_elem_t; the rest of the shape is in the arguments.
+cudaError_t launch_quant_q8(const QuantArgs& a, int x_dtype, bool e5m2, bool block, cudaStream_t st);
+cudaError_t launch_matmul_q8(const MatmulArgs& a, cudaStream_t st);
+
 cudaError_t launch_layout(bool to_hp, const void* in, void* out, int64_t N, int64_t H, int32_t T,
                           int elem_bytes, cudaStream_t stream);
 

@@ -2,17 +2,26 @@
 
 Every function named like a C entry point (``sp_rs_dropout_residual_norm_fwd``,
 ``sp_rs_bwd_workspace_bytes``, ``sp_rs_dropout_residual_norm_bwd``, ``sp2hp``,
-``hp2sp``) passes tensor pointers, sizes and the current CUDA stream to the
+``hp2sp``, ``sp_quantize_q8``, ``sp_matmul_q8``) passes tensor pointers, sizes and the current CUDA stream to the
 function of the same name in ``libspfuse.so`` and raises ``RuntimeError`` with
 the library's status string when it reports an error.  All arithmetic runs in
 the library's CUDA kernels; there is no other implementation to fall back to:
 if the library is missing, the first call raises.
 
 ``forward`` / ``backward`` / ``sp2hp_out`` / ``hp2sp_out`` are conveniences
-that allocate the outputs with torch (device memory only) and call the above.
+that allocate the outputs with torch (device memory only) and call the above;
+so are ``forward_q8``, ``quantize_q8``, ``matmul_q8`` and
+``linear_q8_backward``, the 8-bit operators behind the norm.
+
+An 8-bit tensor is a pair: values ([R, C], ``torch.float8_e4m3fn`` or
+``torch.float8_e5m2``) and scale bytes ([R, ceil(C/128)] ``torch.uint8``, or
+[ceil(R/128), ceil(C/128)] for 128 x 128 blocks; a byte b stands for
+2^(b - 127), as ``torch.float8_e8m0fnu`` reads it).  Both have row strides of
+a multiple of 16 bytes (``q8_empty`` allocates such a matrix).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -25,6 +34,9 @@ SP_RMSNORM, SP_LAYERNORM = 0, 1
 DTYPE_CODE = {torch.float32: SP_F32, torch.bfloat16: SP_BF16}
 NAME_CODE = {"f32": SP_F32, "bf16": SP_BF16}
 NORM_CODE = {"rms": SP_RMSNORM, "ln": SP_LAYERNORM}
+ELEM_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.float8_e5m2: 3}
+Q8_DTYPE = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+Q8_GROUP = 128
 
 
 class SpRsDesc(ctypes.Structure):
@@ -55,6 +67,21 @@ class SpKernelPlan(ctypes.Structure):
 class SpPlanInfo(ctypes.Structure):
     """Mirror of sp_plan_info_t (include/spfuse.h)."""
     _fields_ = [("fwd", SpKernelPlan), ("bwd", SpKernelPlan)]
+
+
+class SpQuantizeQ8Desc(ctypes.Structure):
+    """Mirror of sp_quantize_q8_desc_t (include/spfuse.h)."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("M", "K", "ldx", "ldx_scale", "ldq", "ldq_scale", "ldqt",
+                                              "ldqt_scale")] + \
+               [(n, ctypes.c_int32) for n in ("x_dtype", "q_dtype", "x_scale_rows", "block")] + \
+               [("reserved", ctypes.c_int64)]
+
+
+class SpMatmulQ8Desc(ctypes.Structure):
+    """Mirror of sp_matmul_q8_desc_t (include/spfuse.h)."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("M", "N", "K", "lda", "ldb", "lda_scale", "ldb_scale", "ldc")] + \
+               [(n, ctypes.c_int32) for n in ("a_dtype", "b_dtype", "c_dtype", "a_scale_rows", "b_scale_rows",
+                                              "accumulate")] + [("status", ctypes.c_void_p)]
 
 
 def make_desc(T, j, S, B, H, dtype="bf16", norm="rms", p=0.0, eps=1e-6, seed=0, nshards=1,
@@ -96,6 +123,15 @@ def lib() -> ctypes.CDLL:
         L.sp_rs_dropout_residual_norm_bwd_rows.restype = ctypes.c_int
         L.sp_rs_dropout_residual_norm_bwd_rows.argtypes = [D, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp,
                                                            vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+        L.sp_rs_dropout_residual_norm_fwd_q8.restype = ctypes.c_int
+        L.sp_rs_dropout_residual_norm_fwd_q8.argtypes = [D, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp]
+        L.sp_rs_dropout_residual_norm_fwd_q8_rows.restype = ctypes.c_int
+        L.sp_rs_dropout_residual_norm_fwd_q8_rows.argtypes = [D, i64, i64, vp, vp, vp, vp, vp, vp, i64, vp, i64,
+                                                              vp, vp, vp, vp]
+        L.sp_quantize_q8.restype = ctypes.c_int
+        L.sp_quantize_q8.argtypes = [ctypes.POINTER(SpQuantizeQ8Desc), vp, vp, vp, vp, vp, vp, vp]
+        L.sp_matmul_q8.restype = ctypes.c_int
+        L.sp_matmul_q8.argtypes = [ctypes.POINTER(SpMatmulQ8Desc), vp, vp, vp, vp, vp, vp]
         for name in ("sp2hp", "hp2sp"):
             f = getattr(L, name)
             f.restype = ctypes.c_int
@@ -128,6 +164,19 @@ def _ptr(t):
     if not t.is_contiguous():
         raise ValueError("libspfuse takes dense row-major tensors")
     return t.data_ptr()
+
+
+def _addr(t):
+    return t if t is None or isinstance(t, int) else t.data_ptr()
+
+
+def _rows2d(t):
+    """Address and row stride (elements) of a matrix with dense rows."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("libspfuse takes matrices with dense rows")
+    return t.data_ptr(), max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
 
 
 def _stream(stream):
@@ -217,6 +266,39 @@ def hp2sp(inp, out, N, H, T, dtype, stream=None) -> None:
     _check(lib().hp2sp(_ptr(inp), _ptr(out), N, H, T, NAME_CODE.get(dtype, dtype), _stream(stream)))
 
 
+def sp_rs_dropout_residual_norm_fwd_q8(desc: SpRsDesc, partials, residual, gamma, beta, h_out, q_out, scale_out,
+                                       mask_out, rstd_out, mean_out, stream=None) -> None:
+    arr = (ctypes.c_void_p * max(1, len(partials)))(*[_ptr(p) for p in partials])
+    q, ldq = _rows2d(q_out)
+    s, lds = _rows2d(scale_out)
+    _check(lib().sp_rs_dropout_residual_norm_fwd_q8(
+        ctypes.byref(desc), arr, _ptr(residual), _ptr(gamma), _ptr(beta), _ptr(h_out), q, ldq, s, lds,
+        _ptr(mask_out), _ptr(rstd_out), _ptr(mean_out), _stream(stream)))
+
+
+def sp_rs_dropout_residual_norm_fwd_q8_rows(desc: SpRsDesc, row_begin: int, row_count: int, partials, residual,
+                                            gamma, beta, h_out, q_out, scale_out, mask_out, rstd_out, mean_out,
+                                            stream=None) -> None:
+    arr = (ctypes.c_void_p * max(1, len(partials)))(*[_ptr(p) for p in partials])
+    q, ldq = _rows2d(q_out)
+    s, lds = _rows2d(scale_out)
+    _check(lib().sp_rs_dropout_residual_norm_fwd_q8_rows(
+        ctypes.byref(desc), int(row_begin), int(row_count), arr, _ptr(residual), _ptr(gamma), _ptr(beta),
+        _ptr(h_out), q, ldq, s, lds, _ptr(mask_out), _ptr(rstd_out), _ptr(mean_out), _stream(stream)))
+
+
+def sp_quantize_q8(desc: SpQuantizeQ8Desc, x, x_scale, q, q_scale, qt, qt_scale, stream=None) -> None:
+    """Pointers or tensors; the strides are the descriptor's."""
+    _check(lib().sp_quantize_q8(ctypes.byref(desc), _addr(x), _addr(x_scale), _addr(q), _addr(q_scale), _addr(qt),
+                                _addr(qt_scale), _stream(stream)))
+
+
+def sp_matmul_q8(desc: SpMatmulQ8Desc, a, a_scale, b, b_scale, c, stream=None) -> None:
+    """Pointers or tensors; the strides are the descriptor's."""
+    _check(lib().sp_matmul_q8(ctypes.byref(desc), _addr(a), _addr(a_scale), _addr(b), _addr(b_scale), _addr(c),
+                              _stream(stream)))
+
+
 # ---- conveniences that allocate outputs ------------------------------------------
 
 def forward(desc: SpRsDesc, partials, residual, gamma, beta=None, stream=None,
@@ -270,3 +352,170 @@ def hp2sp_out(x: torch.Tensor, stream=None) -> torch.Tensor:
     out = torch.empty((N, Hc * T), device=x.device, dtype=x.dtype)
     hp2sp(x, out, N, Hc * T, T, DTYPE_CODE[x.dtype], stream)
     return out
+
+
+# ---- the 8-bit operators -----------------------------------------------------------
+
+def q8_empty(rows: int, cols: int, device, dtype=torch.uint8) -> torch.Tensor:
+    """An uninitialised [rows, cols] matrix of one-byte values whose rows start
+    a multiple of 16 bytes apart, as the 8-bit operators take them."""
+    t = torch.empty((rows, max(16, (cols + 15) // 16 * 16)), device=device, dtype=dtype)
+    return t if t.shape[1] == cols else t[:, :cols]
+
+
+def _groups(n: int) -> int:
+    return (n + Q8_GROUP - 1) // Q8_GROUP
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The tensors' device and the caller's stream as the current ones, so that
+    outputs and intermediates are allocated for the stream that uses them."""
+    if stream is None:
+        with torch.cuda.device(device):
+            yield
+        return
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+def _same_device(first, *others):
+    if not first.is_cuda:
+        raise ValueError("libspfuse takes CUDA tensors")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: all must be on one device")
+
+
+def _q8_operand(name, t, scale):
+    """(address, row stride, scales' address, their row stride, rows per scale) of an 8-bit tensor."""
+    if t.dtype not in (torch.float8_e4m3fn, torch.float8_e5m2):
+        raise ValueError(f"{name}: float8_e4m3fn or float8_e5m2 expected, got {t.dtype}")
+    if t.dim() != 2 or scale is None or scale.dim() != 2 or scale.element_size() != 1:
+        raise ValueError(f"{name}: a matrix and its matrix of scale bytes expected")
+    rows, groups = t.shape[0], _groups(t.shape[1])
+    if scale.shape[1] != groups or scale.shape[0] not in (rows, _groups(rows)):
+        raise ValueError(f"{name}: values {tuple(t.shape)} do not go with scales {tuple(scale.shape)}")
+    p, ld = _rows2d(t)
+    s, lds = _rows2d(scale)
+    if rows <= 1 or groups == 0:  # the stride is not used, and a view may carry any
+        ld, lds = (ld + 15) // 16 * 16, (lds + 15) // 16 * 16
+    elif scale.shape[0] == 1:
+        lds = (lds + 15) // 16 * 16
+    return p, ld, s, lds, 1 if scale.shape[0] == rows else Q8_GROUP
+
+
+def forward_q8(desc: SpRsDesc, partials, residual, gamma, beta=None, stream=None, store_mask: bool = True) -> dict:
+    """`forward` with the norm's output in e4m3: `q` [rows, H] and `scale`
+    [rows, ceil(H/128)] in the place of `y`.  `backward` takes the rest."""
+    rows, H = desc.rows, desc.H
+    dev, dt = residual.device, residual.dtype
+    _same_device(residual, gamma, beta, *partials)
+    if DTYPE_CODE.get(dt) != desc.dtype or any(t.dtype != dt for t in (*partials, gamma)):
+        raise ValueError("the tensors' types do not match the descriptor")
+    if len(partials) != desc.T or residual.numel() != rows * H or gamma.numel() != H or \
+            any(t.numel() != desc.S * desc.B * H for t in partials):
+        raise ValueError("the tensors' sizes do not match the descriptor")
+    if desc.norm == SP_LAYERNORM and (beta is None or beta.dtype != dt or beta.numel() != H):
+        raise ValueError("LayerNorm needs beta, as gamma")
+    with _on(dev, stream):
+        out = dict(h=torch.empty((rows, H), device=dev, dtype=dt),
+                   q=q8_empty(rows, H, dev, torch.float8_e4m3fn),
+                   scale=q8_empty(rows, _groups(H), dev),
+                   mask=torch.empty((rows, H), device=dev, dtype=torch.uint8)
+                   if desc.p > 0 and store_mask else None,
+                   rstd=torch.empty(rows, device=dev, dtype=torch.float32),
+                   mean=torch.empty(rows, device=dev, dtype=torch.float32)
+                   if desc.norm == SP_LAYERNORM else None)
+        arr = (ctypes.c_void_p * len(partials))(*[_ptr(p) for p in partials])
+        q, s = out["q"], out["scale"]
+        _check(lib().sp_rs_dropout_residual_norm_fwd_q8(
+            ctypes.byref(desc), arr, _ptr(residual), _ptr(gamma), _ptr(beta), out["h"].data_ptr(), q.data_ptr(),
+            (H + 15) // 16 * 16, s.data_ptr(), (s.shape[1] + 15) // 16 * 16, _ptr(out["mask"]),
+            out["rstd"].data_ptr(), _ptr(out["mean"]), _stream(None)))
+    return out
+
+
+def quantize_q8(x: torch.Tensor, fmt: str = "e4m3", block: bool = False, rowwise: bool = True, colwise: bool = False,
+                scale: torch.Tensor | None = None, stream=None) -> dict:
+    """x [M, K] (float32, bfloat16, or 8-bit values with their `scale` bytes) to
+    8 bits: `q`, `scale` along its rows and/or `qt` [K, M], `scale_t` along its
+    columns (the transposed tensor); with `block` one scale per 128 x 128 block.
+    Outputs not asked for are None."""
+    if x.dim() != 2 or x.dtype not in ELEM_CODE or fmt not in Q8_DTYPE:
+        raise ValueError("a matrix of float32, bfloat16 or 8-bit values and a format e4m3 or e5m2 expected")
+    if not rowwise and not colwise:
+        raise ValueError("neither rowwise nor colwise: nothing to do")
+    _same_device(x, scale)
+    M, K = x.shape
+    d = SpQuantizeQ8Desc(M=M, K=K, x_dtype=ELEM_CODE[x.dtype], q_dtype=ELEM_CODE[Q8_DTYPE[fmt]], block=int(block))
+    if d.x_dtype >= 2:
+        px, d.ldx, ps, d.ldx_scale, d.x_scale_rows = _q8_operand("x", x, scale)
+    else:
+        if scale is not None:
+            raise ValueError("only an 8-bit x has scales")
+        px, d.ldx = _rows2d(x)
+        ps = None
+    q = s = qt = st = None
+    with _on(x.device, stream):
+        if rowwise:
+            q = q8_empty(M, K, x.device, Q8_DTYPE[fmt])
+            s = q8_empty(_groups(M) if block else M, _groups(K), x.device)
+            d.ldq, d.ldq_scale = (K + 15) // 16 * 16, (s.shape[1] + 15) // 16 * 16
+        if colwise:
+            qt = q8_empty(K, M, x.device, Q8_DTYPE[fmt])
+            st = q8_empty(_groups(K) if block else K, _groups(M), x.device)
+            d.ldqt, d.ldqt_scale = (M + 15) // 16 * 16, (st.shape[1] + 15) // 16 * 16
+        if M > 0 and K > 0:
+            sp_quantize_q8(d, px, ps, q, s, qt, st)
+    return dict(q=q, scale=s, qt=qt, scale_t=st)
+
+
+def matmul_q8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+              out: torch.Tensor | None = None, out_dtype=torch.bfloat16, accumulate: bool = False,
+              stream=None, status=None) -> torch.Tensor:
+    """a [M, K] times b [N, K] transposed, both 8-bit tensors, to [M, N] of
+    `out_dtype` (bfloat16 or float32); into `out` when given (its type then
+    counts), added to what a float32 `out` holds with `accumulate`."""
+    if accumulate and out is None:
+        raise ValueError("accumulate needs the out to add to")
+    _same_device(a, a_scale, b, b_scale, out)
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise ValueError("a [M, K] and b [N, K] expected")
+    M, K, N = a.shape[0], a.shape[1], b.shape[0]
+    d = SpMatmulQ8Desc(M=M, N=N, K=K, a_dtype=ELEM_CODE.get(a.dtype, -1), b_dtype=ELEM_CODE.get(b.dtype, -1),
+                       accumulate=int(accumulate), status=_ptr(status))
+    pa, d.lda, psa, d.lda_scale, d.a_scale_rows = _q8_operand("a", a, a_scale)
+    pb, d.ldb, psb, d.ldb_scale, d.b_scale_rows = _q8_operand("b", b, b_scale)
+    with _on(a.device, stream):
+        if out is None:
+            out = torch.empty((M, N), device=a.device, dtype=out_dtype)
+        elif tuple(out.shape) != (M, N):
+            raise ValueError(f"out is {tuple(out.shape)}, the product {(M, N)}")
+        if out.dtype not in DTYPE_CODE:
+            raise ValueError("out: bfloat16 or float32 expected")
+        d.c_dtype = DTYPE_CODE[out.dtype]
+        pc, d.ldc = _rows2d(out)
+        if M > 0 and N > 0:
+            sp_matmul_q8(d, pa, psa, pb, psb, pc)
+    return out
+
+
+def linear_q8_backward(dy: torch.Tensor, x_q: torch.Tensor, x_scale: torch.Tensor, wt_q: torch.Tensor,
+                       wt_scale: torch.Tensor, fmt: str = "e4m3", dw: torch.Tensor | None = None,
+                       dx_dtype=torch.bfloat16, stream=None) -> dict:
+    """Gradients of y = x W^T from dy [M, N] (float32 or bfloat16): `dx` [M, K]
+    = dy W and `dw` [N, K] = dy^T x (float32; added to the given `dw`).  x_q
+    [M, K] is the forward's 8-bit input, wt_q [K, N] the transposed weight
+    (quantize_q8's qt).  dy goes to 8 bits (`fmt`) along N for dx and along its
+    tokens for dw, where x is requantised along its tokens too."""
+    with _on(dy.device, stream):
+        g = quantize_q8(dy, fmt, rowwise=True, colwise=True)
+        xt = quantize_q8(x_q, "e5m2" if x_q.dtype == torch.float8_e5m2 else "e4m3", rowwise=False, colwise=True,
+                         scale=x_scale)
+        dx = matmul_q8(g["q"], g["scale"], wt_q, wt_scale, out_dtype=dx_dtype)
+        dw = matmul_q8(g["qt"], g["scale_t"], xt["qt"], xt["scale_t"], out=dw, out_dtype=torch.float32,
+                       accumulate=dw is not None)
+    return dict(dx=dx, dw=dw)

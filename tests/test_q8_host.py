@@ -1,0 +1,176 @@
+"""Host-side checks of the 8-bit entry points (no GPU): what they refuse, the
+descriptors' layout and the calls that launch nothing."""
+import ctypes
+import os
+import subprocess
+import sys
+import textwrap
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 1 << 20   # a 16-byte aligned address that is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def spf():
+    from residual_sp_rs_gb300 import build, ops
+    build.build()
+    return ops
+
+
+def test_struct_layout_matches_header(spf):
+    assert ctypes.sizeof(spf.SpQuantizeQ8Desc) == 88 and spf.SpQuantizeQ8Desc.x_dtype.offset == 64
+    assert ctypes.sizeof(spf.SpMatmulQ8Desc) == 96 and spf.SpMatmulQ8Desc.a_dtype.offset == 64
+    assert spf.SpMatmulQ8Desc.status.offset == 88
+
+
+# ---- the region's forward with an 8-bit norm output ------------------------------
+
+def _fwd(spf, H=64, ldq=64, lds=16, q=FAKE, scale=FAKE, h=FAKE, dtype="bf16", rows=None, **kw):
+    d = spf.make_desc(2, 0, kw.pop("S", 16), 2, H, dtype, "rms", 0.1, 1e-6)
+    arr = (ctypes.c_void_p * 2)(FAKE, FAKE)
+    L = spf.lib()
+    if rows is None:
+        return L.sp_rs_dropout_residual_norm_fwd_q8(ctypes.byref(d), arr, FAKE, FAKE, None, h, q, ldq, scale, lds,
+                                                    FAKE, FAKE, None, None)
+    return L.sp_rs_dropout_residual_norm_fwd_q8_rows(ctypes.byref(d), *rows, arr, FAKE, FAKE, None, h, q, ldq, scale,
+                                                     lds, FAKE, FAKE, None, None)
+
+
+def test_fwd_q8_refusals(spf):
+    assert _fwd(spf) in (0, 6)                    # valid (6 = no GPU here)
+    assert _fwd(spf, S=15) == 2                   # the region's own checks
+    assert _fwd(spf, H=12) == 2
+    assert _fwd(spf, ldq=48) == 2                 # shorter than H
+    assert _fwd(spf, ldq=72) == 2                 # no multiple of 16
+    assert _fwd(spf, ldq=1 << 62) == 2
+    assert _fwd(spf, lds=8) == 2
+    assert _fwd(spf, lds=0) == 2
+    assert _fwd(spf, H=64 * 33, ldq=64 * 33, lds=16) == 2  # 17 groups
+    assert _fwd(spf, q=0) == 1 and _fwd(spf, scale=0) == 1 and _fwd(spf, h=0) == 1
+    assert _fwd(spf, q=FAKE + 8) == 3 and _fwd(spf, scale=FAKE + 1) == 3
+    assert _fwd(spf, S=0, q=0, scale=0) == 0      # no rows: nothing checked or touched
+    assert _fwd(spf, rows=(0, 17)) == 1 and _fwd(spf, rows=(-1, 2)) == 1
+    assert _fwd(spf, rows=(16, 0), q=0) == 0
+    assert _fwd(spf, rows=(3, 5)) in (0, 6)
+
+
+# ---- quantisation ------------------------------------------------------------------
+
+def _quant(spf, x=FAKE, xs=None, q=FAKE, qs=FAKE, qt=FAKE, qts=FAKE, **kw):
+    f = dict(M=100, K=72, ldx=72, ldx_scale=16, ldq=80, ldq_scale=16, ldqt=112, ldqt_scale=16, x_dtype=1, q_dtype=2,
+             x_scale_rows=0, block=0, reserved=0)
+    f.update(kw)
+    d = spf.SpQuantizeQ8Desc(**f)
+    return spf.lib().sp_quantize_q8(ctypes.byref(d), x, xs, q, qs, qt, qts, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x_dtype=4), 4), (dict(x_dtype=-1), 4), (dict(q_dtype=0), 4), (dict(q_dtype=1), 4), (dict(q_dtype=4), 4),
+    (dict(block=2), 1), (dict(reserved=1), 1), (dict(x_dtype=2, xs=FAKE, ldx=80), 1),
+    (dict(M=-1), 2), (dict(K=-1), 2), (dict(M=1 << 31), 2), (dict(K=1 << 31, ldx=1 << 31), 2),
+    (dict(ldx=71), 2), (dict(ldx=1 << 60), 2), (dict(ldq=64), 2), (dict(ldq=72), 2), (dict(ldq_scale=1), 2),
+    (dict(ldqt=96), 2), (dict(ldqt=104), 2), (dict(ldqt_scale=8), 2),
+    (dict(M=(1 << 31) - 1, K=(1 << 31) - 1, ldx=(1 << 31), ldq=1 << 31, ldqt=1 << 31), 2),
+    (dict(x_dtype=2, xs=FAKE, ldx=72, x_scale_rows=1), 2),       # an 8-bit x needs 16-byte strides
+    (dict(x_dtype=2, xs=FAKE, ldx=80, x_scale_rows=1, ldx_scale=4), 2),
+    (dict(x=None), 1), (dict(x_dtype=2, ldx=80, x_scale_rows=1), 1), (dict(qs=None), 1), (dict(qts=None), 1),
+    (dict(q=None, qt=None), 1),
+    (dict(x=FAKE + 1), 3), (dict(x_dtype=0, x=FAKE + 2), 3), (dict(q=FAKE + 8), 3), (dict(qt=FAKE + 4), 3),
+    (dict(qs=FAKE + 1), 3), (dict(qts=FAKE + 2), 3),
+    (dict(x_dtype=3, xs=FAKE + 1, ldx=80, x_scale_rows=1), 3), (dict(x_dtype=3, x=FAKE + 8, xs=FAKE, ldx=80, x_scale_rows=1), 3),
+])
+def test_quantize_refusals(spf, kw, code):
+    assert _quant(spf, **kw) == code
+
+
+def test_quantize_accepts(spf):
+    for kw in [dict(), dict(q=None, qs=None, ldq=0, ldq_scale=0), dict(qt=None, qts=None, ldqt=0, ldqt_scale=0),
+               dict(block=1), dict(x_dtype=0, x=FAKE + 4), dict(x=FAKE + 2),
+               dict(x_dtype=3, xs=FAKE, ldx=80, x_scale_rows=128)]:
+        assert _quant(spf, **kw) in (0, 6), kw
+    assert _quant(spf, M=0, x=None, qs=None, qts=None) == 0
+    assert _quant(spf, K=0, x=None, qs=None, qts=None) == 0
+    assert spf.lib().sp_quantize_q8(None, FAKE, None, FAKE, FAKE, None, None, None) == 1
+
+
+# ---- the product -------------------------------------------------------------------
+
+def _mm(spf, a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, c=FAKE, **kw):
+    f = dict(M=5, N=7, K=200, lda=208, ldb=208, lda_scale=16, ldb_scale=16, ldc=7, a_dtype=2, b_dtype=3, c_dtype=1,
+             a_scale_rows=1, b_scale_rows=128, accumulate=0, status=None)
+    f.update(kw)
+    d = spf.SpMatmulQ8Desc(**f)
+    return spf.lib().sp_matmul_q8(ctypes.byref(d), a, sa, b, sb, c, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(a_dtype=1), 4), (dict(b_dtype=0), 4), (dict(a_dtype=4), 4), (dict(c_dtype=2), 4),
+    (dict(accumulate=1), 4), (dict(accumulate=2), 1), (dict(a_scale_rows=0), 1), (dict(b_scale_rows=64), 1),
+    (dict(M=-1), 2), (dict(N=-1), 2), (dict(K=-1), 2), (dict(M=1 << 31), 2), (dict(N=1 << 31, ldc=1 << 31), 2),
+    (dict(K=1 << 31, lda=1 << 31, ldb=1 << 31), 2), (dict(lda=192), 2), (dict(lda=200), 2), (dict(ldb=201), 2),
+    (dict(ldb=1 << 61), 2), (dict(lda_scale=1), 2), (dict(ldb_scale=17), 2), (dict(ldc=6), 2), (dict(ldc=1 << 60), 2),
+    (dict(a=None), 1), (dict(sa=None), 1), (dict(b=None), 1), (dict(sb=None), 1), (dict(c=None), 1),
+    (dict(a=FAKE + 8), 3), (dict(sa=FAKE + 4), 3), (dict(b=FAKE + 1), 3), (dict(sb=FAKE + 8), 3), (dict(c=FAKE + 1), 3),
+    (dict(c=FAKE + 2, c_dtype=0), 3), (dict(status=FAKE + 2), 3),
+])
+def test_matmul_refusals(spf, kw, code):
+    assert _mm(spf, **kw) == code
+
+
+def test_matmul_accepts(spf):
+    for kw in [dict(), dict(c=FAKE + 2), dict(c_dtype=0, accumulate=1, c=FAKE + 4), dict(ldc=9),
+               dict(K=0, a=None, b=None, sa=None, sb=None), dict(status=FAKE + 4)]:
+        assert _mm(spf, **kw) in (0, 6), kw
+    assert _mm(spf, M=0, a=None, c=None) == 0
+    assert _mm(spf, N=0, b=None, c=None) == 0
+    assert spf.lib().sp_matmul_q8(None, FAKE, FAKE, FAKE, FAKE, FAKE, None) == 1
+
+
+def test_launch_failure_is_reported(spf):
+    code = textwrap.dedent(f"""
+        import sys
+        sys.path.insert(0, {ROOT!r})
+        from residual_sp_rs_gb300 import ops as spf
+        from tests import test_q8_host as t
+        print(t._fwd(spf), t._quant(spf), t._mm(spf))
+    """)
+    out = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, SPFUSE_FAIL_LAUNCH="1"),
+                         capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0, out.stderr
+    assert out.stdout.split() == ["6", "6", "6"]
+
+
+# ---- the binding ---------------------------------------------------------------------
+
+def test_binding_refuses_what_it_cannot_pass_on(spf):
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        spf.quantize_q8(x)
+    with pytest.raises(ValueError, match="expected"):
+        spf.quantize_q8(x.double())
+    with pytest.raises(ValueError, match="expected"):
+        spf.quantize_q8(x, fmt="e3m4")
+    with pytest.raises(ValueError, match="nothing"):
+        spf.quantize_q8(x, rowwise=False)
+    a, s = torch.zeros(4, 256, dtype=f8), torch.zeros(4, 2, dtype=u8)
+    with pytest.raises(ValueError, match="CUDA"):
+        spf.matmul_q8(a, s, a, s)
+    with pytest.raises(ValueError, match="out to add to"):
+        spf.matmul_q8(a, s, a, s, accumulate=True)
+    for values, scales in [(a, s[:3]), (a, torch.zeros(4, 1, dtype=u8)), (a, s.float()), (a, None), (a.float(), s)]:
+        with pytest.raises(ValueError):
+            spf._q8_operand("a", values, scales)
+    with pytest.raises(ValueError, match="dense rows"):
+        spf._q8_operand("a", torch.zeros(256, 4, dtype=f8).t(), s)
+    assert spf._q8_operand("a", a, s[:1])[4] == 128   # one row of scales for four rows: a block
+    assert spf._q8_operand("a", a, s)[4] == 1
+
+
+def test_q8_empty_strides(spf):
+    for cols in (0, 1, 15, 16, 17, 128):
+        t = spf.q8_empty(3, cols, "cpu")
+        assert t.shape == (3, cols) and t.stride(0) % 16 == 0 and t.stride(0) >= cols
