@@ -185,8 +185,10 @@ sp_status_t sp_rs_dropout_residual_norm_fwd_rows(const sp_rs_desc_t* desc,
  * all-gather in front of that): sp_rs_dropout_residual_norm_fwd with y
  * quantised to e4m3, one scale per token and 128 columns, straight from its
  * fp32 value.  With T = 1 and p = 0 it is the residual's addition and the norm.
- * Everything else (h_out, mask_out, rstd_out, mean_out) is as in that call,
- * bit for bit, so sp_rs_dropout_residual_norm_bwd is its backward too (y's
+ * A bf16 h is the sum's fp32 value rounded to bf16, so it can differ from
+ * that call's by one step where the exact sum lies within half an fp32 step
+ * of a bf16 midpoint; the norm is of the stored h either way.  mask_out is
+ * the same and sp_rs_dropout_residual_norm_bwd is its backward too (y's
  * rounding is passed straight through, as that of a 16-bit y is).
  *
  * q_out: [nshards*R, H] e4m3, ldq bytes between rows; scale_out: [nshards*R,

@@ -290,6 +290,54 @@ __device__ __forceinline__ uint32_t residual_bf2(f2_t res, f2_t acc, f2_t s_hi, 
   return bl | (bh << 16);
 }
 
+// Residual stream of one 16-byte vector for the instances whose y leaves in
+// 8 bits: E = res + acc*(s_hi + s_lo) rounded to fp32 and that to bf16.  The
+// second rounding can only differ from the single one above where E is within
+// half an fp32 step of a bf16 midpoint, so h is off by at most 1/2 + 2^-16
+// bf16 steps: behind a norm that goes on to 8 bits the exact tie decision
+// would cost a quarter more instructions and buy nothing.
+// With c the bf16 truncation of fl(res + acc*s_hi), res - c is exact (8-bit
+// significands; the exponents are close unless the sum cancels), so t is E - c
+// to 2^-32 of E and c + t is E rounded to fp32.  Where the sum cancels or is
+// not finite (inf - inf inside t would turn an infinity into NaN) the plain
+// sum is taken, with acc*s_lo added.
+__device__ __forceinline__ void residual_vec8_via_f32(const f2_t (&acc)[4], const f2_t (&res)[4], f2_t s_hi,
+                                                      f2_t s_lo, uint32_t (&hw)[4]) {
+  bool risky = false;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const f2_t h1 = f2_fma(acc[q], s_hi, res[q]);
+    float hl, hh, rl, rh, el, eh, gl, gh;
+    f2_split(h1, hl, hh);
+    const f2_t c = f2(__uint_as_float(__float_as_uint(hl) & 0xFFFF0000u),
+                      __uint_as_float(__float_as_uint(hh) & 0xFFFF0000u));
+    const f2_t e = f2_add(c, f2_fma(acc[q], s_lo, f2_fma(acc[q], s_hi, f2_sub(res[q], c))));
+    hw[q] = f2_to_bf2(e);
+    f2_split(f2_mul(h1, f2(0x1p12f, 0x1p12f)), gl, gh);
+    f2_split(res[q], rl, rh);
+    f2_split(e, el, eh);
+    risky |= fabsf(gl) < fabsf(rl) || fabsf(gh) < fabsf(rh) || !(fabsf(el) < 0x1p127f) || !(fabsf(eh) < 0x1p127f);
+  }
+  if (risky) {
+    float shl, shh, sll, slh;
+    f2_split(s_hi, shl, shh);
+    f2_split(s_lo, sll, slh);
+    auto plain = [&](float r, float a, uint32_t bits) -> uint32_t {
+      const float h1 = __fmaf_rn(a, shl, r);
+      if (fabsf(h1) * 0x1p12f >= fabsf(r) && fabsf(h1) < 0x1p126f) return bits;
+      const __nv_bfloat16 b = __float2bfloat16_rn(isfinite(h1) ? __fmaf_rn(a, sll, h1) : h1);
+      return (uint32_t) * reinterpret_cast<const unsigned short*>(&b);
+    };
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float al, ah, rl, rh;
+      f2_split(acc[q], al, ah);
+      f2_split(res[q], rl, rh);
+      hw[q] = plain(rl, al, hw[q] & 0xFFFFu) | (plain(rh, ah, hw[q] >> 16) << 16);
+    }
+  }
+}
+
 // Mask bytes <-> keep bits.  Bit 0 of every mask byte is the keep flag (the
 // forward writes 0 or 1).  Four bits spread to four bytes with one multiply
 // (the shifted copies 0, 7, 14, 21 do not overlap), and four bytes gather

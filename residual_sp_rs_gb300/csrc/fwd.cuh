@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(512) sp_fwd_kernel(const FwdArgs a) {
       if constexpr (EV == 8) {
         const f2_t shi = f2(a.scale, a.scale), slo = f2(a.scale_lo, a.scale_lo);
         uint32_t hw[4];
+        f2_t accs[4], ress[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t* p0 = reinterpret_cast<const uint32_t*>(&pv[k][0]);
@@ -91,7 +92,13 @@ __global__ void __launch_bounds__(512) sp_fwd_kernel(const FwdArgs a) {
           float al, ah;
           f2_split(acc, al, ah);
           acc = f2(((keep >> (2 * i)) & 1u) ? al : 0.f, ((keep >> (2 * i + 1)) & 1u) ? ah : 0.f);
-          hw[i] = residual_bf2(bf2_to_f2(reinterpret_cast<const uint32_t*>(&rv[k])[i]), acc, shi, slo);
+          accs[i] = acc;
+          ress[i] = bf2_to_f2(reinterpret_cast<const uint32_t*>(&rv[k])[i]);
+          if constexpr (!Q8) hw[i] = residual_bf2(ress[i], acc, shi, slo);
+        }
+        if constexpr (Q8) residual_vec8_via_f32(accs, ress, shi, slo, hw);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           hf[k][i] = bf2_to_f2(hw[i]);  // the norm reads the stored (rounded) value
           s2 = LN ? f2_add(s2, hf[k][i]) : f2_fma(hf[k][i], hf[k][i], s2);
         }

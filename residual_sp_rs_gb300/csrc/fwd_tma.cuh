@@ -27,7 +27,7 @@
 // Q8: y leaves in e4m3 with a scale byte per 128 columns instead of bf16.  A
 // group is 16 neighbouring lanes' vectors (its maximum is four shuffles); the
 // fp32 value of y is scaled and rounded to 8 bits at once, without the
-// rounding to bf16 in between.
+// rounding to bf16 in between.  h is rounded through fp32 (residual_vec8_via_f32).
 //
 // If a wait times out, the row group stops, writes NaN into the rstd of the
 // rows it did not finish and reports the timeout in the device status word.
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(NTHR, 1) sp_fwd_tma_kernel(const FwdArgs a, co
         const uint4 rw = reinterpret_cast<const uint4*>(sb + (size_t)T * L.blk)[vi];
         const uint32_t kb = keep[k];
         uint32_t hw[4];
-        if constexpr (FAST) {
+        if constexpr (FAST || Q8) {  // Q8 without dropout: every keep bit is set
           f2_t acc[4], res[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -358,7 +358,10 @@ __global__ void __launch_bounds__(NTHR, 1) sp_fwd_tma_kernel(const FwdArgs a, co
             acc[q] = f2(((kb >> (2 * q)) & 1u) ? al : 0.f, ((kb >> (2 * q + 1)) & 1u) ? ah : 0.f);
             res[q] = bf2_to_f2(reinterpret_cast<const uint32_t*>(&rw)[q]);
           }
-          residual_vec8_drop(acc, res, shi, slo, hw);
+          if constexpr (Q8)
+            residual_vec8_via_f32(acc, res, shi, slo, hw);
+          else
+            residual_vec8_drop(acc, res, shi, slo, hw);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f2_t hq = bf2_to_f2(hw[q]);

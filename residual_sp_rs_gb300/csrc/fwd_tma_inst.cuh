@@ -25,8 +25,10 @@ inline void (*fwd_tma_kernel_for_vpt(int vpt))(const FwdArgs, const FwdTmaLayout
 
 template <bool LN, int T, int NTHR, bool CH, bool Q8>
 inline void (*fwd_tma_kernel_for_mode(int vpt, bool fast))(const FwdArgs, const FwdTmaLayout) {
-  return fast ? fwd_tma_kernel_for_vpt<LN, T, true, NTHR, CH, Q8>(vpt)
-              : fwd_tma_kernel_for_vpt<LN, T, false, NTHR, CH, Q8>(vpt);
+  // with y in 8 bits h's rounding has no tie rule and the modes do not differ
+  if constexpr (!Q8)
+    if (fast) return fwd_tma_kernel_for_vpt<LN, T, true, NTHR, CH, false>(vpt);
+  return fwd_tma_kernel_for_vpt<LN, T, false, NTHR, CH, Q8>(vpt);
 }
 
 template <bool LN, int T, bool CH, bool Q8>

@@ -367,10 +367,11 @@ def _groups(n: int) -> int:
     return (n + Q8_GROUP - 1) // Q8_GROUP
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 @contextlib.contextmanager
-def _on(device, stream):
-    """The tensors' device and the caller's stream as the current ones, so that
-    outputs and intermediates are allocated for the stream that uses them."""
+def _on_stream(device, stream):
     if stream is None:
         with torch.cuda.device(device):
             yield
@@ -379,6 +380,14 @@ def _on(device, stream):
         stream = torch.cuda.ExternalStream(stream, device=device)
     with torch.cuda.device(device), torch.cuda.stream(stream):
         yield
+
+
+def _on(device, stream):
+    """The tensors' device and the caller's stream as the current ones, so that
+    outputs and intermediates are allocated for the stream that uses them."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _NOTHING
+    return _on_stream(device, stream)
 
 
 def _same_device(first, *others):
