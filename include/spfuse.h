@@ -96,6 +96,7 @@ typedef struct sp_rs_desc_t {
  * likes (e.g. once per training step).  A clean run leaves it unchanged. */
 #define SP_DEVICE_FWD_WAIT_TIMEOUT 0x1u /* a forward kernel gave up waiting */
 #define SP_DEVICE_BWD_WAIT_TIMEOUT 0x2u /* a backward kernel gave up waiting */
+#define SP_DEVICE_MATMUL_WAIT_TIMEOUT 0x4u /* sp_matmul_q8 gave up waiting; unfinished tiles of C are NaN */
 
 /* Forward of the SP region for sequence shards j .. j+nshards-1.
  *

@@ -558,7 +558,12 @@ sp_status_t sp_matmul_q8(const sp_matmul_q8_desc_t* d, const uint8_t* a, const u
   m.a_e5m2 = d->a_dtype == SP_ELEM_E5M2;
   m.b_e5m2 = d->b_dtype == SP_ELEM_E5M2;
   m.c_f32 = d->c_dtype == SP_ELEM_F32;
+  const int64_t cb = m.c_f32 ? 4 : 2;
+  m.c_vec = aligned(c, 16) && d->ldc * cb % 16 == 0;
   m.accumulate = d->accumulate;
+  m.status = d->status;
+  m.wait_ns = wait_hooks().wait_ns;
+  m.drop_stage = wait_hooks().drop_stage;
   if (inject_launch_failure()) return SP_ERR_CUDA;
   return from_cuda(launch_matmul_q8(m, reinterpret_cast<cudaStream_t>(stream)));
 }

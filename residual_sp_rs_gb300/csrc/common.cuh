@@ -518,12 +518,17 @@ struct MatmulArgs {
   int32_t a_scale_rows, b_scale_rows;  // rows that share a scale: 1 or 128
   int32_t a_e5m2, b_e5m2;
   int32_t c_f32;
+  int32_t c_vec;            // C's rows allow 16-byte accesses
   int32_t accumulate;
+  uint32_t* status;         // device status word (timeouts are ORed in) or null
+  uint64_t wait_ns;         // bound of every mbarrier wait
+  int32_t drop_stage;       // test hook: CTA 0's producer never fills this stage (-1: none)
 };
 
 // Bits of the device status word (the values of include/spfuse.h).
 constexpr uint32_t kStatusFwdWaitTimeout = 0x1u;
 constexpr uint32_t kStatusBwdWaitTimeout = 0x2u;
+constexpr uint32_t kStatusMatmulWaitTimeout = 0x4u;
 
 __device__ __forceinline__ void report_status(uint32_t* status, uint32_t bit) {
   if (status) atomicOr(status, bit);

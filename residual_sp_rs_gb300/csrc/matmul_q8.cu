@@ -1,72 +1,521 @@
 // matmul_q8.cu -- C = A B^T of 8-bit tensors with a power-of-two scale per 128
-// values along K.
+// values along K, on the 5th-generation tensor cores.
 //
-//   C[i,j] = sum_k (2^sa[i,k/128] qa[i,k]) (2^sb[j,k/128] qb[j,k]),
+//   C[i,j] = sum_k (2^sa[i,k/128] qa[i,k]) (2^sb[j,k/128] qb[j,k])
 //
-// both factors exact in fp32, sums in fp32, one rounding to C's type.  64 x 64
-// tiles of C, 16 columns of K a step through shared memory, 4 x 4 sums a
-// thread.
+// The tensor core applies the scales itself (kind mxf8f6f4: a ue8m0 byte per
+// row and 32 values of K; the four 32-value steps of a 128-value block use
+// the same byte) and keeps the whole sum over K in fp32 in tensor memory, so
+// nothing is rounded before C's own type.
+//
+// A CTA (CG = 1) or a pair of CTAs (CG = 2) works on one tile: 128 rows of
+// the X operand per CTA against BN rows of the Y operand.  X is A and Y is B,
+// or the other way round (SWAP) when A has few rows: then the weights fill
+// the tensor core's 128 rows and the tokens its short side.
+//   warp 0     producer: one 128-byte wide tile of X and of Y per stage, by
+//              tiled bulk copies into a ring of stages (128-byte swizzle)
+//   warp 1     issues the tensor core instructions (and owns tensor memory)
+//   warps 2-3  bring the scale bytes: per 4 blocks of K one 32-bit word per
+//              row, into the 32 x 16 byte layout that goes to tensor memory
+//   warps 4-7  epilogue: tensor memory to C
+// Tiles are dealt to the resident CTAs in turn; the two accumulators in tensor
+// memory let the epilogue of one tile run under the products of the next.
+// Few tiles (decoding): `ks` CTAs of a cluster split K and add their fp32
+// sums through distributed shared memory in rank order, so the result does not
+// depend on timing.
+//
+// Every wait is bounded (tma.cuh); a role that gives up reports it in the
+// status word, the tiles that were not finished are written as NaN, and tensor
+// memory is freed after the instructions and copies in flight are done.
+#include <cuda.h>
+
 #include "common.cuh"
 #include "launch.h"
 #include "q8.cuh"
+#include "umma.cuh"
 
 namespace spf {
 
 namespace {
 
-constexpr int kTile = 64, kStep = 16;
+constexpr int kThreads = 256;
+constexpr int kXRows = 128;                   // rows of X per CTA
+constexpr uint32_t kXBytes = kXRows * 128;    // one stage of X
+constexpr int kMaxStages = 12;
+constexpr int kScaleSlots = 4;                // ring of scale words, 4 blocks of K each
+constexpr uint32_t kScaleAtom = 512;          // 128 rows x 4 scale bytes
 
-__device__ __forceinline__ float element(const uint8_t* p, const uint8_t* scale, int64_t ld, int64_t lds, int srows,
-                                         bool e5m2, int64_t row, int64_t rows, int64_t k, int64_t K) {
-  if (row >= rows || k >= K) return 0.f;
-  float lo, hi;
-  q8_unpack2(p[row * ld + k], e5m2, lo, hi);
-  return lo * q8_scale(scale[row / srows * lds + (k >> 7)]);
+struct MatmulPlan {
+  int32_t BN;            // rows of Y per tile, a multiple of 16 (32 for CG = 2), at most 256
+  int32_t stages;
+  int32_t ks;            // CTAs that split K (CG = 1)
+  int32_t xtiles, ytiles;
+  int32_t nkb;           // 128-value blocks of K
+  uint32_t tmem_cols;    // power of two
+  uint32_t acc1;         // column of the second accumulator
+  uint32_t sf_col;       // first column of the scales
+  uint32_t smem;
+};
+
+struct Shared {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t sf_full[kScaleSlots], sf_empty[kScaleSlots];
+  uint64_t acc_full, acc_free, drain;
+  uint32_t tmem;
+};
+
+__host__ __device__ constexpr uint32_t scale_atoms_y(int BN) { return (uint32_t)(BN + 127) / 128; }
+
+// Tile t of the list: columns of 16 X tiles, along Y within them, so that the
+// tiles in flight share their operands in L2.
+__device__ __forceinline__ void tile_at(const MatmulPlan& p, int64_t t, int CG, int64_t& tx, int64_t& ty) {
+  const int64_t w = 16 / CG, per = w * p.ytiles, g = t / per, in = t - g * per;
+  const int64_t width = min(w, (int64_t)p.xtiles - g * w);
+  tx = g * w + in % width;
+  ty = in / width;
 }
 
-__global__ void __launch_bounds__(256) sp_matmul_q8_kernel(const MatmulArgs a) {
-  __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-  const int64_t ntiles = (a.N + kTile - 1) / kTile;
-  const int64_t m0 = blockIdx.x / ntiles * kTile, n0 = blockIdx.x % ntiles * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+template <int CG, bool SWAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    sp_matmul_q8_kernel(const MatmulArgs a, const MatmulPlan p, const __grid_constant__ CUtensorMap mapx,
+                        const __grid_constant__ CUtensorMap mapy) {
+  extern __shared__ __align__(1024) unsigned char dsm_raw[];
+  __shared__ Shared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 || p.ks > 1 ? cluster_rank() : 0;
+  const bool leader = CG == 1 || rank == 0;  // of the CTA pair
+  const uint32_t base = (smem_addr(dsm_raw) + 1023u) & ~1023u;
+  unsigned char* dsm = dsm_raw + (base - smem_addr(dsm_raw));
+  const uint32_t ybytes = (uint32_t)(p.BN / CG) * 128u, stage_bytes = kXBytes + ybytes;
+  const uint32_t sf_bytes = kScaleAtom * (1 + scale_atoms_y(p.BN));
+  const uint32_t sf_base = base + (uint32_t)p.stages * stage_bytes;
+
+  // X is the operand whose rows fill the tensor core's 128 lanes
+  const int64_t XR = SWAP ? a.N : a.M, YR = SWAP ? a.M : a.N;
+  const int64_t xt_pairs = p.xtiles;  // tiles of CG * 128 rows
+  const int64_t tiles = xt_pairs * p.ytiles;
+  const int group = CG * p.ks;                          // CTAs per tile
+  const int64_t first = blockIdx.x / group, step = gridDim.x / group;
+  const int split = CG == 1 ? (int)rank : 0;
+  const int kb0 = (int)((int64_t)p.nkb * split / p.ks), kb1 = (int)((int64_t)p.nkb * (split + 1) / p.ks);
+
+  if (warp == 0 && lane == 0) {
+    if (p.nkb > 0) {
+      prefetch_tensor_map(&mapx);
+      prefetch_tensor_map(&mapy);
+    }
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) {
+      mbar_init(&sh.sf_full[s], 2 * CG);
+      mbar_init(&sh.sf_empty[s], 1);
+    }
+    mbar_init(&sh.acc_full, 1);
+    mbar_init(&sh.acc_free, 4 * CG);
+    mbar_init(&sh.drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc<CG>(&sh.tmem, p.tmem_cols);
+  tmem_fence_before();
+  if (CG == 2 || p.ks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = sh.tmem;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < a.K; k0 += kStep) {
-    for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-      const int r = i / kStep, k = i % kStep;
-      sa[k][r] = element(a.a, a.a_scale, a.lda, a.lda_scale, a.a_scale_rows, a.a_e5m2, m0 + r, a.M, k0 + k, a.K);
-      sb[k][r] = element(a.b, a.b_scale, a.ldb, a.ldb_scale, a.b_scale_rows, a.b_e5m2, n0 + r, a.N, k0 + k, a.K);
+
+  const uint64_t limit = a.wait_ns;
+  if (warp == 0) {
+    // ---- producer -------------------------------------------------------------
+    if (lane == 0) {
+      int s = 0, issued = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t t = first; t < tiles && ok; t += step) {
+        int64_t tx, ty;
+        tile_at(p, t, CG, tx, ty);
+        const int32_t x0 = (int32_t)(tx * CG + (CG == 2 ? rank : 0)) * kXRows;
+        const int32_t y0 = (int32_t)(ty * p.BN) + (CG == 2 ? (int32_t)rank * (p.BN / 2) : 0);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait_cluster(&sh.empty[s], ph ^ 1u, limit)) {
+            ok = false;
+            break;
+          }
+          if (!(issued == a.drop_stage && blockIdx.x == 0)) {  // test hook: this stage never lands
+            const uint32_t st = base + (uint32_t)s * stage_bytes;
+            uint32_t bar = smem_addr(&sh.full[s]);
+            if (leader) mbar_arrive_expect_tx(&sh.full[s], stage_bytes * CG);
+            if (CG == 2) bar = map_cta(bar, 0);
+            tma_load_2d<CG>(st, &mapx, kb * 128, x0, bar);
+            tma_load_2d<CG>(st + kXBytes, &mapy, kb * 128, y0, bar);
+          }
+          ++issued;
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok) report_status(a.status, kStatusMatmulWaitTimeout);
+      // nothing may still be landing in shared memory when the CTA exits; the
+      // leader's barriers count the pair's copies
+      if (leader)
+        for (int j = max(0, issued - p.stages); j < issued; ++j)
+          mbar_wait_cluster(&sh.full[j % p.stages], (uint32_t)(j / p.stages) & 1u, limit);
     }
-    __syncthreads();
+  } else if (warp == 1) {
+    // ---- tensor core instructions ------------------------------------------------
+    if (lane == 0 && leader) {
+      const uint32_t idesc = idesc_mxf8(SWAP ? a.b_e5m2 : a.a_e5m2, SWAP ? a.a_e5m2 : a.b_e5m2, kXRows * CG, p.BN);
+      const uint32_t sfx = tmem + p.sf_col, sfy = sfx + 4;
+      int s = 0, q = 0;
+      uint32_t ph = 0, qph = 0;
+      uint32_t n = 0;  // tiles of this CTA so far
+      bool ok = true;
+      for (int64_t t = first; t < tiles && ok; t += step, ++n) {
+        const uint32_t d = tmem + (n & 1u ? p.acc1 : 0u);
+        // the accumulators may overlap in the columns that the epilogue of
+        // the tile before reads first; it has finished the tile before that
+        if (n > 0 && !mbar_wait_cluster(&sh.acc_free, (n - 1) & 1u, limit)) {
+          ok = false;
+          break;
+        }
+        tmem_fence_after();
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (kb == kb0 || (kb & 3) == 0) {
+            if (!mbar_wait_cluster(&sh.sf_full[q], qph, limit)) {
+              ok = false;
+              break;
+            }
+            tmem_fence_after();
+            const uint32_t src = sf_base + (uint32_t)q * sf_bytes;
+            tmem_cp_scales<CG>(sfx, desc_rows16(src));
+            for (uint32_t i = 0; i < scale_atoms_y(p.BN); ++i)
+              tmem_cp_scales<CG>(sfy + 4 * i, desc_rows16(src + kScaleAtom * (1 + i)));
+            umma_commit<CG>(&sh.sf_empty[q]);
+            if (++q == kScaleSlots) {
+              q = 0;
+              qph ^= 1u;
+            }
+          }
+          if (!mbar_wait_cluster(&sh.full[s], ph, limit)) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          const uint32_t st = base + (uint32_t)s * stage_bytes;
+          const uint64_t dx = desc_sw128(st), dy = desc_sw128(st + kXBytes);
+          const uint32_t id = idesc_scale_byte(idesc, (uint32_t)kb & 3u);
+          const int64_t left = a.K - (int64_t)kb * 128;
+          const int steps = left >= 128 ? 4 : (int)((left + 31) >> 5);
+          for (int i = 0; i < steps; ++i)  // 32 bytes of K a step: 2 in the descriptor's units
+            umma_mxf8<CG>(d, dx + 2 * i, dy + 2 * i, id, sfx, sfy, kb > kb0 || i > 0);
+          umma_commit<CG>(&sh.empty[s]);
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) umma_commit<CG>(&sh.acc_full);
+      }
+      if (!ok) report_status(a.status, kStatusMatmulWaitTimeout);
+      umma_commit<CG>(&sh.drain);
+      mbar_wait_cluster(&sh.drain, 0, limit);  // nothing in flight when tensor memory is freed
+    }
+  } else if (warp < 4) {
+    // ---- scales -------------------------------------------------------------------
+    const int tid = threadIdx.x - 64;
+    const uint8_t* xs = SWAP ? a.b_scale : a.a_scale;
+    const uint8_t* ys = SWAP ? a.a_scale : a.b_scale;
+    const int64_t xld = SWAP ? a.ldb_scale : a.lda_scale, yld = SWAP ? a.lda_scale : a.ldb_scale;
+    const int xshift = (SWAP ? a.b_scale_rows : a.a_scale_rows) == 1 ? 0 : 7;
+    const int yshift = (SWAP ? a.a_scale_rows : a.b_scale_rows) == 1 ? 0 : 7;
+    int q = 0;
+    uint32_t qph = 0;
+    bool ok = true;
+    for (int64_t t = first; t < tiles && ok; t += step) {
+      int64_t tx, ty;
+      tile_at(p, t, CG, tx, ty);
+      const int64_t x0 = (tx * CG + (CG == 2 ? rank : 0)) * kXRows, y0 = ty * p.BN;
+      for (int g = kb0 >> 2; g <= (kb1 - 1) >> 2 && kb0 < kb1; ++g) {
+        uint32_t w[6];
 #pragma unroll
-    for (int k = 0; k < kStep; ++k)
+        for (int i = 0; i < 6; ++i) {  // rows tid, tid + 64, ... of X (128), then of Y
+          const int r = tid + 64 * i - (i < 2 ? 0 : kXRows);
+          const int64_t row = (i < 2 ? x0 : y0) + r;
+          w[i] = 0x7F7F7F7Fu;  // rows outside the tensor: zeros times one
+          if (i < 2 ? row < XR : r < p.BN && row < YR)
+            w[i] = __ldg(reinterpret_cast<const uint32_t*>(i < 2 ? xs + (row >> xshift) * xld : ys + (row >> yshift) * yld) + g);
+        }
+        if (!mbar_wait_cluster(&sh.sf_empty[q], qph ^ 1u, limit)) {
+          ok = false;
+          break;
+        }
+        unsigned char* dst = dsm + (uint32_t)p.stages * stage_bytes + (uint32_t)q * sf_bytes;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][ty + 16 * i] * sb[k][tx + 16 * j];
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= a.M || n >= a.N) continue;
-      if (a.c_f32) {
-        float* p = static_cast<float*>(a.c) + m * a.ldc + n;
-        *p = a.accumulate ? *p + acc[i][j] : acc[i][j];
-      } else {
-        static_cast<__nv_bfloat16*>(a.c)[m * a.ldc + n] = __float2bfloat16_rn(acc[i][j]);
+        for (int i = 0; i < 6; ++i) {
+          const int r = tid + 64 * i;  // row r & 127 of atom r >> 7
+          if (r < 128 * (1 + (int)scale_atoms_y(p.BN)))
+            *reinterpret_cast<uint32_t*>(dst + (r >> 7) * kScaleAtom + (r & 31) * 16 + ((r & 127) >> 5) * 4) = w[i];
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2)
+            mbar_arrive_cluster(map_cta(smem_addr(&sh.sf_full[q]), 0));
+          else
+            mbar_arrive(&sh.sf_full[q]);
+        }
+        if (++q == kScaleSlots) {
+          q = 0;
+          qph ^= 1u;
+        }
       }
     }
+    if (!ok && tid == 0) report_status(a.status, kStatusMatmulWaitTimeout);
+  } else {
+    // ---- epilogue -----------------------------------------------------------------
+    const int w4 = warp & 3;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int64_t t = first; t < tiles; t += step, ++n) {
+      int64_t tx, ty;
+      tile_at(p, t, CG, tx, ty);
+      const int64_t x = (tx * CG + (CG == 2 ? rank : 0)) * kXRows + 32 * w4 + lane, y0 = ty * p.BN;
+      const uint32_t acc = tmem + (n & 1u ? p.acc1 : 0u) + ((uint32_t)(32 * w4) << 16);
+      if (kb0 < kb1 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&sh.acc_full, n & 1u, limit));
+      if (!ok && lane == 0 && w4 == 0) report_status(a.status, kStatusMatmulWaitTimeout);
+      tmem_fence_after();
+      const int chunks = (p.BN + 31) / 32;
+      for (int c = 0; c < chunks; ++c) {
+        // the columns that the accumulators may share come first
+        const int col = 32 * (n & 1u ? c : chunks - 1 - c);
+        uint32_t v[32];
+        if (kb0 < kb1 && ok) {
+          if (p.BN - col >= 32) {
+            tmem_ld32(acc + col, v);
+          } else {
+            uint32_t u[16];
+            tmem_ld16(acc + col, u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = u[i];
+          }
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = ok ? 0u : 0x7FC00000u;
+        }
+        if (c == 0) {
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 2)
+              mbar_arrive_cluster(map_cta(smem_addr(&sh.acc_free), 0));
+            else
+              mbar_arrive(&sh.acc_free);
+          }
+        }
+        const int64_t y = y0 + col;
+        const int ny = (int)min((int64_t)min(32, p.BN - col), YR - y);  // columns inside C
+        if (p.ks > 1) {
+          float* part = reinterpret_cast<float*>(dsm) + col * kXRows + 32 * w4 + lane;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i < ny) part[i * kXRows] = __uint_as_float(v[i]);
+        } else if (x < XR) {
+          if constexpr (SWAP) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (i >= ny) continue;
+              const int64_t o = (y + i) * a.ldc + x;
+              if (a.c_f32) {
+                float* c1 = static_cast<float*>(a.c) + o;
+                *c1 = __uint_as_float(v[i]) + (a.accumulate ? *c1 : 0.f);
+              } else {
+                static_cast<__nv_bfloat16*>(a.c)[o] = __float2bfloat16_rn(__uint_as_float(v[i]));
+              }
+            }
+          } else if (a.c_f32) {
+            float* c1 = static_cast<float*>(a.c) + x * a.ldc + y;
+            if (a.c_vec && ny == 32) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float4* c4 = reinterpret_cast<float4*>(c1 + i);
+                float4 o = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
+                                       __uint_as_float(v[i + 3]));
+                if (a.accumulate) {
+                  const float4 b = *c4;
+                  o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
+                }
+                *c4 = o;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < ny) c1[i] = __uint_as_float(v[i]) + (a.accumulate ? c1[i] : 0.f);
+            }
+          } else {
+            __nv_bfloat16* c1 = static_cast<__nv_bfloat16*>(a.c) + x * a.ldc + y;
+            if (a.c_vec && ny == 32) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[i + e]);
+                *reinterpret_cast<uint4*>(c1 + i) = Act16<__nv_bfloat16>::pack(f);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < ny) c1[i] = __float2bfloat16_rn(__uint_as_float(v[i]));
+            }
+          }
+        }
+      }
+    }
+    tmem_fence_before();
+  }
+  __syncwarp();
+
+  // ---- the cluster's sums over K, in rank order ------------------------------------
+  if (CG == 2) {
+    cluster_sync();
+  } else if (p.ks > 1) {
+    cluster_sync();  // one tile per cluster: every CTA's part is in its shared memory
+    if constexpr (SWAP) {
+      int64_t tx, ty;
+      tile_at(p, first, CG, tx, ty);
+      const int l = threadIdx.x & 127;
+      const int64_t x = tx * kXRows + l;
+      const int cols = (int)min((int64_t)p.BN, YR - ty * p.BN);
+      for (int col = (int)rank + p.ks * (threadIdx.x >> 7); col < cols; col += 2 * p.ks) {
+        float sum = 0.f;
+        for (int r = 0; r < p.ks; ++r) sum += ld_cluster_f32(map_cta(base + (uint32_t)(col * kXRows + l) * 4u, r));
+        if (x < XR) {
+          const int64_t o = (ty * p.BN + col) * a.ldc + x;
+          if (a.c_f32) {
+            float* c1 = static_cast<float*>(a.c) + o;
+            *c1 = sum + (a.accumulate ? *c1 : 0.f);
+          } else {
+            static_cast<__nv_bfloat16*>(a.c)[o] = __float2bfloat16_rn(sum);
+          }
+        }
+      }
+    }
+    cluster_sync();  // nobody's shared memory goes before it is read
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tmem_fence_after();
+    tmem_dealloc<CG>(tmem, p.tmem_cols);
+  }
+}
+
+// cuTensorMapEncodeTiled of the loaded driver.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encode_tiled(EncodeTiled* out) {
+  static void* fn = nullptr;  // the same pointer whoever looks it up
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+    fn = f;
+  }
+  *out = reinterpret_cast<EncodeTiled>(fn);
+  return cudaSuccess;
+}
+
+// [rows, K] bytes, `ld` apart, in boxes of 128 bytes x `box` rows.
+cudaError_t operand_map(const void* p, int64_t rows, int64_t K, int64_t ld, int box, CUtensorMap* map) {
+  EncodeTiled encode;
+  const cudaError_t e = encode_tiled(&encode);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, ones[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, boxes, ones,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+uint32_t pow2_at_least(uint32_t n) {
+  uint32_t c = 32;
+  while (c < n) c *= 2;
+  return c;
+}
+
+template <int CG, bool SWAP>
+cudaError_t launch(const MatmulArgs& a, MatmulPlan p, int sms, cudaStream_t st) {
+  CUtensorMap mx = {}, my = {};
+  if (p.nkb > 0) {
+    const int64_t XR = SWAP ? a.N : a.M, YR = SWAP ? a.M : a.N;
+    cudaError_t e = operand_map(SWAP ? a.b : a.a, XR, a.K, SWAP ? a.ldb : a.lda, kXRows, &mx);
+    if (e == cudaSuccess) e = operand_map(SWAP ? a.a : a.b, YR, a.K, SWAP ? a.lda : a.ldb, p.BN / CG, &my);
+    if (e != cudaSuccess) return e;
+  }
+  auto k = sp_matmul_q8_kernel<CG, SWAP>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)p.xtiles * p.ytiles;
+  const int group = CG * p.ks;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.ks > 1 ? tiles : min(tiles, (int64_t)(sms / CG))) * group));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)group;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = group > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k, a, p, mx, my);
 }
 
 }  // namespace
 
 cudaError_t launch_matmul_q8(const MatmulArgs& a, cudaStream_t st) {
-  const int64_t tiles = ((a.M + kTile - 1) / kTile) * ((a.N + kTile - 1) / kTile);
-  return pdl_launch(sp_matmul_q8_kernel, dim3((unsigned)tiles), dim3(256), 0, st, a);
+  int dev = 0, sms = 0, optin = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e != cudaSuccess) return e;
+
+  MatmulPlan p = {};
+  p.nkb = (int32_t)((a.K + 127) / 128);
+  const bool swap = a.M <= 64;
+  const int64_t XR = swap ? a.N : a.M, YR = swap ? a.M : a.N;
+  p.BN = swap ? (int32_t)((YR + 15) / 16 * 16) : YR > 128 ? 256 : 128;
+  p.xtiles = (int32_t)((XR + kXRows - 1) / kXRows);
+  p.ytiles = (int32_t)((YR + p.BN - 1) / p.BN);
+  p.ks = 1;
+  if (swap) {
+    // a cluster per tile, K split until the SMs are filled twice
+    while (p.ks < 8 && p.ks * 2 <= p.nkb && (int64_t)p.xtiles * p.ytiles * p.ks < sms) p.ks *= 2;
+  }
+  const uint32_t sf_cols = 16;  // 4 for X and 4 or 8 for Y; every start a multiple of 16
+  p.tmem_cols = pow2_at_least((p.ks > 1 ? p.BN : 2 * p.BN) + sf_cols);
+  if (p.tmem_cols > 512) p.tmem_cols = 512;
+  p.sf_col = p.tmem_cols - sf_cols;
+  p.acc1 = p.sf_col - p.BN;  // overlaps the first accumulator by less than 32 columns
+  const uint32_t stage = kXBytes + (uint32_t)p.BN * 128u, fixed = 1024 + 1024 + kScaleSlots * kScaleAtom * (1 + scale_atoms_y(p.BN));
+  p.stages = (int32_t)((optin - fixed) / stage);
+  if (p.stages > 8) p.stages = 8;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.smem = 1024 + p.stages * stage + kScaleSlots * kScaleAtom * (1 + scale_atoms_y(p.BN));
+  return swap ? launch<1, true>(a, p, sms, st) : launch<1, false>(a, p, sms, st);
 }
 
 }  // namespace spf
