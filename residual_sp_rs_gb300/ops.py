@@ -174,14 +174,15 @@ def _rows2d(t):
     """Address and row stride (elements) of a matrix with dense rows."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError("libspfuse takes matrices with dense rows")
-    return t.data_ptr(), max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], shape[1])
 
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -359,8 +360,11 @@ def hp2sp_out(x: torch.Tensor, stream=None) -> torch.Tensor:
 def q8_empty(rows: int, cols: int, device, dtype=torch.uint8) -> torch.Tensor:
     """An uninitialised [rows, cols] matrix of one-byte values whose rows start
     a multiple of 16 bytes apart, as the 8-bit operators take them."""
-    t = torch.empty((rows, max(16, (cols + 15) // 16 * 16)), device=device, dtype=dtype)
-    return t if t.shape[1] == cols else t[:, :cols]
+    return torch.empty_strided((rows, cols), (_ld16(cols), 1), dtype=dtype, device=device)
+
+
+def _ld16(n: int) -> int:
+    return (n + 15) // 16 * 16 or 16
 
 
 def _groups(n: int) -> int:
@@ -385,66 +389,73 @@ def _on_stream(device, stream):
 def _on(device, stream):
     """The tensors' device and the caller's stream as the current ones, so that
     outputs and intermediates are allocated for the stream that uses them."""
-    if stream is None and device.index == torch.cuda.current_device():
+    if stream is None and (device if isinstance(device, int) else device.index) == torch.cuda.current_device():
         return _NOTHING
     return _on_stream(device, stream)
 
 
 def _same_device(first, *others):
-    if not first.is_cuda:
+    """The index of the CUDA device that every tensor is on."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("libspfuse takes CUDA tensors")
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors on {first.device} and {t.device}: all must be on one device")
+    return dev
+
+
+_Q8_CODE = {torch.float8_e4m3fn: 2, torch.float8_e5m2: 3}
+_SCALE_DTYPES = {torch.uint8, torch.float8_e8m0fnu}
 
 
 def _q8_operand(name, t, scale):
     """(address, row stride, scales' address, their row stride, rows per scale) of an 8-bit tensor."""
-    if t.dtype not in (torch.float8_e4m3fn, torch.float8_e5m2):
+    if t.dtype not in _Q8_CODE:
         raise ValueError(f"{name}: float8_e4m3fn or float8_e5m2 expected, got {t.dtype}")
-    if t.dim() != 2 or scale is None or scale.dim() != 2 or scale.element_size() != 1:
+    if scale is None or scale.dtype not in _SCALE_DTYPES or len(scale.shape) != 2 or len(t.shape) != 2:
         raise ValueError(f"{name}: a matrix and its matrix of scale bytes expected")
-    rows, groups = t.shape[0], _groups(t.shape[1])
-    if scale.shape[1] != groups or scale.shape[0] not in (rows, _groups(rows)):
+    (rows, cols), (srows, groups) = t.shape, scale.shape
+    if groups != (cols + 127) // 128 or (srows != rows and srows != (rows + 127) // 128):
         raise ValueError(f"{name}: values {tuple(t.shape)} do not go with scales {tuple(scale.shape)}")
     p, ld = _rows2d(t)
     s, lds = _rows2d(scale)
     if rows <= 1 or groups == 0:  # the stride is not used, and a view may carry any
-        ld, lds = (ld + 15) // 16 * 16, (lds + 15) // 16 * 16
-    elif scale.shape[0] == 1:
-        lds = (lds + 15) // 16 * 16
-    return p, ld, s, lds, 1 if scale.shape[0] == rows else Q8_GROUP
+        ld, lds = _ld16(ld), _ld16(lds)
+    elif srows == 1:
+        lds = _ld16(lds)
+    return p, ld, s, lds, 1 if srows == rows else Q8_GROUP
 
 
 def forward_q8(desc: SpRsDesc, partials, residual, gamma, beta=None, stream=None, store_mask: bool = True) -> dict:
     """`forward` with the norm's output in e4m3: `q` [rows, H] and `scale`
     [rows, ceil(H/128)] in the place of `y`.  `backward` takes the rest."""
-    rows, H = desc.rows, desc.H
-    dev, dt = residual.device, residual.dtype
-    _same_device(residual, gamma, beta, *partials)
-    if DTYPE_CODE.get(dt) != desc.dtype or any(t.dtype != dt for t in (*partials, gamma)):
+    rows, H, T, ln = desc.rows, desc.H, desc.T, desc.norm == SP_LAYERNORM
+    dt = residual.dtype
+    dev = _same_device(residual, gamma, beta, *partials)
+    if DTYPE_CODE.get(dt) != desc.dtype or gamma.dtype != dt:
         raise ValueError("the tensors' types do not match the descriptor")
-    if len(partials) != desc.T or residual.numel() != rows * H or gamma.numel() != H or \
-            any(t.numel() != desc.S * desc.B * H for t in partials):
+    if len(partials) != T or residual.numel() != rows * H or gamma.numel() != H:
         raise ValueError("the tensors' sizes do not match the descriptor")
-    if desc.norm == SP_LAYERNORM and (beta is None or beta.dtype != dt or beta.numel() != H):
+    n = desc.S * desc.B * H
+    for t in partials:
+        if t.dtype != dt or t.numel() != n:
+            raise ValueError("the partials' types or sizes do not match the descriptor")
+    if ln and (beta is None or beta.dtype != dt or beta.numel() != H):
         raise ValueError("LayerNorm needs beta, as gamma")
     with _on(dev, stream):
-        out = dict(h=torch.empty((rows, H), device=dev, dtype=dt),
-                   q=q8_empty(rows, H, dev, torch.float8_e4m3fn),
-                   scale=q8_empty(rows, _groups(H), dev),
-                   mask=torch.empty((rows, H), device=dev, dtype=torch.uint8)
-                   if desc.p > 0 and store_mask else None,
-                   rstd=torch.empty(rows, device=dev, dtype=torch.float32),
-                   mean=torch.empty(rows, device=dev, dtype=torch.float32)
-                   if desc.norm == SP_LAYERNORM else None)
-        arr = (ctypes.c_void_p * len(partials))(*[_ptr(p) for p in partials])
-        q, s = out["q"], out["scale"]
+        cuda = residual.device
+        h = torch.empty((rows, H), device=cuda, dtype=dt)
+        q = q8_empty(rows, H, cuda, torch.float8_e4m3fn)
+        s = q8_empty(rows, _groups(H), cuda)
+        mask = torch.empty((rows, H), device=cuda, dtype=torch.uint8) if store_mask and desc.p > 0 else None
+        rstd = torch.empty(rows, device=cuda, dtype=torch.float32)
+        mean = torch.empty(rows, device=cuda, dtype=torch.float32) if ln else None
         _check(lib().sp_rs_dropout_residual_norm_fwd_q8(
-            ctypes.byref(desc), arr, _ptr(residual), _ptr(gamma), _ptr(beta), out["h"].data_ptr(), q.data_ptr(),
-            (H + 15) // 16 * 16, s.data_ptr(), (s.shape[1] + 15) // 16 * 16, _ptr(out["mask"]),
-            out["rstd"].data_ptr(), _ptr(out["mean"]), _stream(None)))
-    return out
+            ctypes.byref(desc), (ctypes.c_void_p * T)(*[_ptr(p) for p in partials]), _ptr(residual), _ptr(gamma),
+            _ptr(beta), h.data_ptr(), q.data_ptr(), _ld16(H), s.data_ptr(), _ld16(_groups(H)), _ptr(mask),
+            rstd.data_ptr(), _ptr(mean), _stream(None)))
+    return dict(h=h, q=q, scale=s, mask=mask, rstd=rstd, mean=mean)
 
 
 def quantize_q8(x: torch.Tensor, fmt: str = "e4m3", block: bool = False, rowwise: bool = True, colwise: bool = False,
@@ -453,32 +464,35 @@ def quantize_q8(x: torch.Tensor, fmt: str = "e4m3", block: bool = False, rowwise
     8 bits: `q`, `scale` along its rows and/or `qt` [K, M], `scale_t` along its
     columns (the transposed tensor); with `block` one scale per 128 x 128 block.
     Outputs not asked for are None."""
-    if x.dim() != 2 or x.dtype not in ELEM_CODE or fmt not in Q8_DTYPE:
+    xcode, out8 = ELEM_CODE.get(x.dtype, -1), Q8_DTYPE.get(fmt)
+    if len(x.shape) != 2 or xcode < 0 or out8 is None:
         raise ValueError("a matrix of float32, bfloat16 or 8-bit values and a format e4m3 or e5m2 expected")
     if not rowwise and not colwise:
         raise ValueError("neither rowwise nor colwise: nothing to do")
-    _same_device(x, scale)
+    dev = _same_device(x, scale)
     M, K = x.shape
-    d = SpQuantizeQ8Desc(M=M, K=K, x_dtype=ELEM_CODE[x.dtype], q_dtype=ELEM_CODE[Q8_DTYPE[fmt]], block=int(block))
-    if d.x_dtype >= 2:
-        px, d.ldx, ps, d.ldx_scale, d.x_scale_rows = _q8_operand("x", x, scale)
+    ps, ldxs, srows = None, 0, 0
+    if xcode >= 2:
+        px, ldx, ps, ldxs, srows = _q8_operand("x", x, scale)
     else:
         if scale is not None:
             raise ValueError("only an 8-bit x has scales")
-        px, d.ldx = _rows2d(x)
-        ps = None
-    q = s = qt = st = None
-    with _on(x.device, stream):
+        px, ldx = _rows2d(x)
+    mg, kg = _groups(M), _groups(K)
+    q = s = qt = st = pq = pqs = pqt = pqts = None
+    ldq, ldqt = _ld16(K), _ld16(M)
+    with _on(dev, stream):
+        cuda = x.device
         if rowwise:
-            q = q8_empty(M, K, x.device, Q8_DTYPE[fmt])
-            s = q8_empty(_groups(M) if block else M, _groups(K), x.device)
-            d.ldq, d.ldq_scale = (K + 15) // 16 * 16, (s.shape[1] + 15) // 16 * 16
+            q, s = q8_empty(M, K, cuda, out8), q8_empty(mg if block else M, kg, cuda)
+            pq, pqs = q.data_ptr(), s.data_ptr()
         if colwise:
-            qt = q8_empty(K, M, x.device, Q8_DTYPE[fmt])
-            st = q8_empty(_groups(K) if block else K, _groups(M), x.device)
-            d.ldqt, d.ldqt_scale = (M + 15) // 16 * 16, (st.shape[1] + 15) // 16 * 16
+            qt, st = q8_empty(K, M, cuda, out8), q8_empty(kg if block else K, mg, cuda)
+            pqt, pqts = qt.data_ptr(), st.data_ptr()
         if M > 0 and K > 0:
-            sp_quantize_q8(d, px, ps, q, s, qt, st)
+            d = SpQuantizeQ8Desc(M, K, ldx, ldxs, ldq, _ld16(kg), ldqt, _ld16(mg), xcode, ELEM_CODE[out8], srows,
+                                 1 if block else 0, 0)
+            _check(lib().sp_quantize_q8(ctypes.byref(d), px, ps, pq, pqs, pqt, pqts, _stream(None)))
     return dict(q=q, scale=s, qt=qt, scale_t=st)
 
 
@@ -490,25 +504,25 @@ def matmul_q8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: 
     counts), added to what a float32 `out` holds with `accumulate`."""
     if accumulate and out is None:
         raise ValueError("accumulate needs the out to add to")
-    _same_device(a, a_scale, b, b_scale, out)
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
-        raise ValueError("a [M, K] and b [N, K] expected")
-    M, K, N = a.shape[0], a.shape[1], b.shape[0]
-    d = SpMatmulQ8Desc(M=M, N=N, K=K, a_dtype=ELEM_CODE.get(a.dtype, -1), b_dtype=ELEM_CODE.get(b.dtype, -1),
-                       accumulate=int(accumulate), status=_ptr(status))
-    pa, d.lda, psa, d.lda_scale, d.a_scale_rows = _q8_operand("a", a, a_scale)
-    pb, d.ldb, psb, d.ldb_scale, d.b_scale_rows = _q8_operand("b", b, b_scale)
-    with _on(a.device, stream):
+    dev = _same_device(a, a_scale, b, b_scale, out)
+    pa, lda, psa, ldas, asr = _q8_operand("a", a, a_scale)
+    pb, ldb, psb, ldbs, bsr = _q8_operand("b", b, b_scale)
+    (M, K), (N, Kb) = a.shape, b.shape
+    if K != Kb:
+        raise ValueError(f"a [M, K] and b [N, K] expected, got {tuple(a.shape)} and {tuple(b.shape)}")
+    with _on(dev, stream):
         if out is None:
             out = torch.empty((M, N), device=a.device, dtype=out_dtype)
         elif tuple(out.shape) != (M, N):
             raise ValueError(f"out is {tuple(out.shape)}, the product {(M, N)}")
-        if out.dtype not in DTYPE_CODE:
+        code = DTYPE_CODE.get(out.dtype)
+        if code is None:
             raise ValueError("out: bfloat16 or float32 expected")
-        d.c_dtype = DTYPE_CODE[out.dtype]
-        pc, d.ldc = _rows2d(out)
+        pc, ldc = _rows2d(out)
         if M > 0 and N > 0:
-            sp_matmul_q8(d, pa, psa, pb, psb, pc)
+            d = SpMatmulQ8Desc(M, N, K, lda, ldb, ldas, ldbs, ldc, _Q8_CODE[a.dtype], _Q8_CODE[b.dtype], code, asr, bsr,
+                               1 if accumulate else 0, _ptr(status))
+            _check(lib().sp_matmul_q8(ctypes.byref(d), pa, psa, pb, psb, pc, _stream(None)))
     return out
 
 
