@@ -29,6 +29,8 @@
 // memory is freed after the instructions and copies in flight are done.
 #include <cuda.h>
 
+#include <cmath>
+
 #include "common.cuh"
 #include "launch.h"
 #include "q8.cuh"
@@ -44,6 +46,7 @@ constexpr uint32_t kXBytes = kXRows * 128;    // one stage of X
 constexpr int kMaxStages = 12;
 constexpr int kScaleSlots = 4;                // ring of scale words, 4 blocks of K each
 constexpr uint32_t kScaleAtom = 512;          // 128 rows x 4 scale bytes
+constexpr uint32_t kStoreBytes = 4096;        // each epilogue warp's 32 x 32 piece of C
 
 struct MatmulPlan {
   int32_t BN;            // rows of Y per tile, a multiple of 16 (32 for CG = 2), at most 256
@@ -73,6 +76,79 @@ __device__ __forceinline__ void tile_at(const MatmulPlan& p, int64_t t, int CG, 
   const int64_t width = min(w, (int64_t)p.xtiles - g * w);
   tx = g * w + in % width;
   ty = in / width;
+}
+
+__device__ __forceinline__ void store_one(const MatmulArgs& a, int64_t o, float v) {
+  if (a.c_f32) {
+    float* c = static_cast<float*>(a.c) + o;
+    *c = v + (a.accumulate ? *c : 0.f);
+  } else {
+    static_cast<__nv_bfloat16*>(a.c)[o] = __float2bfloat16_rn(v);
+  }
+}
+
+// 32 columns y.. (ny of them inside C) of this warp's 32 rows x.., each lane
+// holding one row, to C: through 4 KB of shared memory (16-byte pieces, their
+// place in a row exclusive-or'ed with the row so that neither side meets a
+// bank conflict), from which neighbouring lanes write neighbouring addresses.
+__device__ __forceinline__ void store_rows(const MatmulArgs& a, unsigned char* buf, int64_t x, int64_t XR, int64_t y,
+                                           int ny, int lane, const uint32_t (&v)[32]) {
+  __syncwarp();  // the piece before this one has been read
+  if (a.c_f32) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+          make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    __syncwarp();
+    float* c = static_cast<float*>(a.c) + x * a.ldc + y;
+    if (a.c_vec && ny == 32) {
+      const int q = lane & 7;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        if (x + r >= XR) continue;
+        float4 o = *reinterpret_cast<const float4*>(buf + r * 128 + ((q ^ (r & 7)) << 4));
+        float4* p = reinterpret_cast<float4*>(c + r * a.ldc + 4 * q);
+        if (a.accumulate) {
+          const float4 b = *p;
+          o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
+        }
+        *p = o;
+      }
+    } else {
+      for (int r = 0; r < 32; ++r) {
+        if (x + r >= XR || lane >= ny) continue;
+        const float o = *reinterpret_cast<const float*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3));
+        float* p = c + r * a.ldc + lane;
+        *p = o + (a.accumulate ? *p : 0.f);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q + e]);
+      *reinterpret_cast<uint4*>(buf + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = Act16<__nv_bfloat16>::pack(f);
+    }
+    __syncwarp();
+    __nv_bfloat16* c = static_cast<__nv_bfloat16*>(a.c) + x * a.ldc + y;
+    if (a.c_vec && ny == 32) {
+      const int q = lane & 3;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        if (x + r < XR)
+          *reinterpret_cast<uint4*>(c + r * a.ldc + 8 * q) =
+              *reinterpret_cast<const uint4*>(buf + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+      }
+    } else {
+      for (int r = 0; r < 32; ++r)
+        if (x + r < XR && lane < ny)
+          c[r * a.ldc + lane] = *reinterpret_cast<const __nv_bfloat16*>(
+              buf + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7));
+    }
+  }
 }
 
 template <int CG, bool SWAP>
@@ -280,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---- epilogue -----------------------------------------------------------------
     const int w4 = warp & 3;
+    unsigned char* stage_c = dsm + (uint32_t)p.stages * stage_bytes + kScaleSlots * sf_bytes + w4 * kStoreBytes;
     uint32_t n = 0;
     bool ok = true;
     for (int64_t t = first; t < tiles; t += step, ++n) {
@@ -326,54 +403,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (i < ny) part[i * kXRows] = __uint_as_float(v[i]);
-        } else if (x < XR) {
-          if constexpr (SWAP) {
+        } else if constexpr (SWAP) {
+          // a lane's columns are rows of C: 32 lanes write neighbouring elements
+          if (x < XR) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (i >= ny) continue;
-              const int64_t o = (y + i) * a.ldc + x;
-              if (a.c_f32) {
-                float* c1 = static_cast<float*>(a.c) + o;
-                *c1 = __uint_as_float(v[i]) + (a.accumulate ? *c1 : 0.f);
-              } else {
-                static_cast<__nv_bfloat16*>(a.c)[o] = __float2bfloat16_rn(__uint_as_float(v[i]));
-              }
-            }
-          } else if (a.c_f32) {
-            float* c1 = static_cast<float*>(a.c) + x * a.ldc + y;
-            if (a.c_vec && ny == 32) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float4* c4 = reinterpret_cast<float4*>(c1 + i);
-                float4 o = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
-                                       __uint_as_float(v[i + 3]));
-                if (a.accumulate) {
-                  const float4 b = *c4;
-                  o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
-                }
-                *c4 = o;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < ny) c1[i] = __uint_as_float(v[i]) + (a.accumulate ? c1[i] : 0.f);
-            }
-          } else {
-            __nv_bfloat16* c1 = static_cast<__nv_bfloat16*>(a.c) + x * a.ldc + y;
-            if (a.c_vec && ny == 32) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[i + e]);
-                *reinterpret_cast<uint4*>(c1 + i) = Act16<__nv_bfloat16>::pack(f);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < ny) c1[i] = __float2bfloat16_rn(__uint_as_float(v[i]));
-            }
+            for (int i = 0; i < 32; ++i)
+              if (i < ny) store_one(a, (y + i) * a.ldc + x, __uint_as_float(v[i]));
           }
+        } else if (ny > 0) {
+          store_rows(a, stage_c, x - lane, XR, y, ny, lane, v);
         }
       }
     }
@@ -395,15 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int col = (int)rank + p.ks * (threadIdx.x >> 7); col < cols; col += 2 * p.ks) {
         float sum = 0.f;
         for (int r = 0; r < p.ks; ++r) sum += ld_cluster_f32(map_cta(base + (uint32_t)(col * kXRows + l) * 4u, r));
-        if (x < XR) {
-          const int64_t o = (ty * p.BN + col) * a.ldc + x;
-          if (a.c_f32) {
-            float* c1 = static_cast<float*>(a.c) + o;
-            *c1 = sum + (a.accumulate ? *c1 : 0.f);
-          } else {
-            static_cast<__nv_bfloat16*>(a.c)[o] = __float2bfloat16_rn(sum);
-          }
-        }
+        if (x < XR) store_one(a, (ty * p.BN + col) * a.ldc + x, sum);
       }
     }
     cluster_sync();  // nobody's shared memory goes before it is read
@@ -454,6 +484,69 @@ uint32_t pow2_at_least(uint32_t n) {
   return c;
 }
 
+struct Choice {
+  int cg;
+  bool swap;
+};
+
+int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
+// Tile shape and split of K: the least of an estimate of the time, in clocks.
+// A block of K costs a CTA the larger of its products (2 BN clocks for 128 x
+// BN x 128) and its loads (its rows of 128 bytes at about kLoadRate a clock);
+// a CTA works off its share of the tiles one after the other, and pays once for
+// starting, for the last tile's epilogue and, with K split, for the join.
+Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
+  constexpr double kLoadRate = 55.0, kStart = 2500.0, kPerColumn = 12.0, kJoin = 1500.0;
+  Choice ch = {1, false};
+  double least = 1e300;
+  const int64_t nkb = ceil_div(a.K, 128);
+  for (int mode = 0; mode < 3; ++mode) {  // one CTA, a pair of CTAs, one CTA with the operands swapped
+    const int cg = mode == 1 ? 2 : 1;
+    const bool swap = mode == 2;
+    const int64_t XR = swap ? a.N : a.M, YR = swap ? a.M : a.N;
+    for (int BN = 256; BN >= 16; BN -= 16) {
+      if (cg == 2 && BN % 32 != 0) continue;
+      if (BN - 16 >= YR && BN > 16 * cg) continue;  // a narrower tile holds every row of Y
+      const int64_t xt = ceil_div(XR, (int64_t)kXRows * cg), yt = ceil_div(YR, BN);
+      for (int ks = 1; ks <= 8; ks *= 2) {
+        // of clusters of 2, 4 and 8 CTAs 152, 144 and 120 CTAs are resident at once on 152 SMs
+        const int64_t room = ks == 8 ? sms * 15 / 19 : ks == 4 ? sms * 18 / 19 : sms;
+        if (ks > 1 && (!swap || ks > nkb || xt * yt * ks > room)) break;
+        const double block = fmax(2.0 * BN, (kXRows + BN / cg) * 128 / kLoadRate);
+        const int64_t turns = ceil_div(xt * yt * ks * cg, sms / cg * cg);
+        const double t = kStart + (double)turns * ceil_div(nkb, ks) * block + kPerColumn * BN + (ks > 1 ? kJoin : 0.0);
+        if (t < least) {
+          least = t;
+          ch = {cg, swap};
+          best->BN = BN;
+          best->ks = ks;
+          best->xtiles = (int32_t)xt;
+          best->ytiles = (int32_t)yt;
+        }
+      }
+    }
+  }
+  MatmulPlan& p = *best;
+  p.nkb = (int32_t)nkb;
+  const uint32_t sf_cols = 16;  // 4 for X and 4 or 8 for Y; every start a multiple of 16
+  p.tmem_cols = pow2_at_least((p.ks > 1 ? p.BN : 2 * p.BN) + sf_cols);
+  if (p.tmem_cols > 512) p.tmem_cols = 512;
+  p.sf_col = p.tmem_cols - sf_cols;
+  p.acc1 = p.sf_col - p.BN;  // overlaps the first accumulator by less than 32 columns
+  const uint32_t stage = kXBytes + (uint32_t)(p.BN / ch.cg) * 128u;
+  const uint32_t rest = 1024 + kScaleSlots * kScaleAtom * (1 + scale_atoms_y(p.BN)) + (ch.swap ? 0 : 4 * kStoreBytes);
+  int64_t stages = ((int64_t)optin - 1024 - rest) / stage;  // 1024: the kernel's static shared memory, rounded up
+  if (stages > kMaxStages) stages = kMaxStages;
+  const int64_t need = ceil_div(nkb, p.ks) * ceil_div((int64_t)p.xtiles * p.ytiles * p.ks * ch.cg, sms);
+  // no more than the CTA ever fills, but room for the join's fp32 sums
+  int64_t least_stages = p.ks > 1 ? ceil_div((int64_t)p.BN * kXRows * 4, stage) : 2;
+  if (need > least_stages) least_stages = need;
+  p.stages = (int32_t)(stages < least_stages ? stages : least_stages);
+  p.smem = rest + p.stages * stage;
+  return ch;
+}
+
 template <int CG, bool SWAP>
 cudaError_t launch(const MatmulArgs& a, MatmulPlan p, int sms, cudaStream_t st) {
   CUtensorMap mx = {}, my = {};
@@ -494,28 +587,9 @@ cudaError_t launch_matmul_q8(const MatmulArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
 
   MatmulPlan p = {};
-  p.nkb = (int32_t)((a.K + 127) / 128);
-  const bool swap = a.M <= 64;
-  const int64_t XR = swap ? a.N : a.M, YR = swap ? a.M : a.N;
-  p.BN = swap ? (int32_t)((YR + 15) / 16 * 16) : YR > 128 ? 256 : 128;
-  p.xtiles = (int32_t)((XR + kXRows - 1) / kXRows);
-  p.ytiles = (int32_t)((YR + p.BN - 1) / p.BN);
-  p.ks = 1;
-  if (swap) {
-    // a cluster per tile, K split until the SMs are filled twice
-    while (p.ks < 8 && p.ks * 2 <= p.nkb && (int64_t)p.xtiles * p.ytiles * p.ks < sms) p.ks *= 2;
-  }
-  const uint32_t sf_cols = 16;  // 4 for X and 4 or 8 for Y; every start a multiple of 16
-  p.tmem_cols = pow2_at_least((p.ks > 1 ? p.BN : 2 * p.BN) + sf_cols);
-  if (p.tmem_cols > 512) p.tmem_cols = 512;
-  p.sf_col = p.tmem_cols - sf_cols;
-  p.acc1 = p.sf_col - p.BN;  // overlaps the first accumulator by less than 32 columns
-  const uint32_t stage = kXBytes + (uint32_t)p.BN * 128u, fixed = 1024 + 1024 + kScaleSlots * kScaleAtom * (1 + scale_atoms_y(p.BN));
-  p.stages = (int32_t)((optin - fixed) / stage);
-  if (p.stages > 8) p.stages = 8;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.smem = 1024 + p.stages * stage + kScaleSlots * kScaleAtom * (1 + scale_atoms_y(p.BN));
-  return swap ? launch<1, true>(a, p, sms, st) : launch<1, false>(a, p, sms, st);
+  const Choice ch = choose_plan(a, sms, optin, &p);
+  if (ch.cg == 2) return launch<2, false>(a, p, sms, st);
+  return ch.swap ? launch<1, true>(a, p, sms, st) : launch<1, false>(a, p, sms, st);
 }
 
 }  // namespace spf

@@ -6,13 +6,14 @@
 // the input once and one byte per element and output.
 //
 // A CTA takes a 128 x 128 tile, in which every group of either direction (and
-// a 128 x 128 block) is whole.  Thread (g, c) of 16 x 16 holds the 8 x 8 block
-// of rows 8g.. and columns 8c.. in registers: a row's maximum is then four
-// shuffles over 16 lanes, a column's one shuffle and a sum over eight warps
-// in shared memory, and the bytes of a column's eight rows form one 8-byte
-// word of the transposed tile.  That tile goes through shared memory (word g
-// of column k at slot g ^ (k / 8), so that neither side meets a bank conflict)
-// and leaves in 128-byte lines.
+// a 128 x 128 block) is whole.  A thread holds the block of its kRows rows and
+// 8 columns in registers: bf16 as packed words, 8 rows; fp32 and 8-bit input as
+// fp32 values, 4 rows, so that 64 registers do and 32 warps fit on an SM.  A
+// row's maximum is then four shuffles over 16 lanes, a column's one shuffle and
+// a maximum over the warps in shared memory, and the bytes of a column's rows
+// form one word of the transposed tile.  That tile goes through shared memory
+// (8-byte word r of column k at slot r ^ (k / 8), so that neither side meets a
+// bank conflict) and leaves 128 bytes of a column at a time.
 #include "common.cuh"
 #include "launch.h"
 #include "q8.cuh"
@@ -21,20 +22,28 @@ namespace spf {
 
 namespace {
 
-constexpr int kQuantThreads = 256;
-
 enum class Src { kF32, kBf16, kQ8 };
 
 template <Src S>
-struct SrcBytes {
-  static constexpr int v = S == Src::kF32 ? 4 : S == Src::kBf16 ? 2 : 1;
+struct Shape {
+  static constexpr int kBytes = S == Src::kF32 ? 4 : S == Src::kBf16 ? 2 : 1;
+  static constexpr int kRows = S == Src::kBf16 ? 8 : 4;      // rows per thread
+  static constexpr int kThreads = 16 * kQ8Group / kRows;
+  static constexpr int kWords = S == Src::kBf16 ? 4 : 8;     // registers per row
 };
 
-// Eight consecutive elements of a row from column `col` on, zero past K.
+// max(a, |b|, |c|) that keeps a NaN.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Eight consecutive elements of a row from column `col` on, zero past K: the
+// raw words, for an 8-bit x the 8 bytes in w[0..1].
 template <Src S>
-__device__ __forceinline__ void load8(const QuantArgs& a, int64_t row, int64_t col, float scale, float (&v)[8]) {
-  const char* p = static_cast<const char*>(a.x) + (row * a.ldx + col) * SrcBytes<S>::v;
-  uint32_t w[8] = {};
+__device__ __forceinline__ void load8(const QuantArgs& a, int64_t row, int64_t col, uint32_t (&w)[Shape<S>::kWords]) {
+  const char* p = static_cast<const char*>(a.x) + (row * a.ldx + col) * Shape<S>::kBytes;
   if (a.vec && col + 8 <= a.K) {
     if constexpr (S == Src::kQ8) {
       const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
@@ -42,7 +51,7 @@ __device__ __forceinline__ void load8(const QuantArgs& a, int64_t row, int64_t c
       w[1] = u.y;
     } else {
 #pragma unroll
-      for (int i = 0; i < SrcBytes<S>::v / 2; ++i) {
+      for (int i = 0; i < Shape<S>::kBytes / 2; ++i) {
         const uint4 u = ld_stream(p + 16 * i);
         w[4 * i] = u.x;
         w[4 * i + 1] = u.y;
@@ -50,35 +59,23 @@ __device__ __forceinline__ void load8(const QuantArgs& a, int64_t row, int64_t c
         w[4 * i + 3] = u.w;
       }
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (col + e >= a.K) continue;
-      if constexpr (S == Src::kF32)
-        w[e] = *(reinterpret_cast<const uint32_t*>(p) + e);
-      else if constexpr (S == Src::kBf16)
-        w[e / 2] |= (uint32_t) * (reinterpret_cast<const uint16_t*>(p) + e) << (16 * (e & 1));
-      else
-        w[e / 4] |= (uint32_t) * (reinterpret_cast<const uint8_t*>(p) + e) << (8 * (e & 3));
-    }
+    return;
   }
-  if constexpr (S == Src::kF32) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
-  } else if constexpr (S == Src::kBf16) {
+  for (int i = 0; i < Shape<S>::kWords; ++i) w[i] = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) Act16<__nv_bfloat16>::unpack_word(w[i], v[2 * i], v[2 * i + 1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q8_unpack2(w[i / 2] >> (16 * (i & 1)), a.x_e5m2 != 0, v[2 * i], v[2 * i + 1]);
-      v[2 * i] *= scale;
-      v[2 * i + 1] *= scale;
-    }
+  for (int e = 0; e < 8; ++e) {
+    if (col + e >= a.K) continue;
+    if constexpr (S == Src::kF32)
+      w[e] = *(reinterpret_cast<const uint32_t*>(p) + e);
+    else if constexpr (S == Src::kBf16)
+      w[e / 2] |= (uint32_t) * (reinterpret_cast<const uint16_t*>(p) + e) << (16 * (e & 1));
+    else
+      w[e / 4] |= (uint32_t) * (reinterpret_cast<const uint8_t*>(p) + e) << (8 * (e & 3));
   }
 }
 
-// Up to eight bytes to p, `n` of them inside the tensor.
+// Up to N (8 or 16) bytes to p, `n` of them inside the tensor.
 __device__ __forceinline__ void store8(uint8_t* p, uint2 w, int64_t n) {
   if (n >= 8) {
     *reinterpret_cast<uint2*>(p) = w;
@@ -88,112 +85,174 @@ __device__ __forceinline__ void store8(uint8_t* p, uint2 w, int64_t n) {
   for (int e = 0; e < 8; ++e)
     if (e < n) p[e] = (uint8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
 }
+__device__ __forceinline__ void store16(uint8_t* p, uint4 w, int64_t n) {
+  if (n >= 16) {
+    *reinterpret_cast<uint4*>(p) = w;
+    return;
+  }
+  store8(p, make_uint2(w.x, w.y), n);
+  store8(p + 8, make_uint2(w.z, w.w), n - 8);
+}
 
 template <Src S, bool E5M2, bool BLOCK>
-__global__ void __launch_bounds__(kQuantThreads) sp_quant_q8_kernel(const QuantArgs a) {
-  __shared__ uint32_t wmax[kQuantThreads / 32][kQ8Group];  // column maxima of each warp
-  __shared__ uint8_t cscale[kQ8Group];
-  __shared__ __align__(16) uint2 tile[kQ8Group * 16];      // transposed bytes
+__global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads) sp_quant_q8_kernel(const QuantArgs a) {
+  constexpr int kRows = Shape<S>::kRows, kThreads = Shape<S>::kThreads, kWarps = kThreads / 32;
+  __shared__ uint32_t wmax[kWarps][kQ8Group];          // column maxima of each warp
+  __shared__ float cinv[kQ8Group];                     // 2^-s of each column
+  __shared__ __align__(16) uint2 tile[kQ8Group * 16];  // transposed bytes
 
-  const int c = threadIdx.x & 15, g = threadIdx.x >> 4, warp = threadIdx.x >> 5;
+  const int c = threadIdx.x & 15, g = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t tm = blockIdx.x / a.ktiles, tk = blockIdx.x - tm * a.ktiles;
-  const int64_t row0 = tm * kQ8Group + 8 * g, col0 = tk * kQ8Group + 8 * c;
+  const int64_t row0 = tm * kQ8Group + kRows * g, col0 = tk * kQ8Group + 8 * c;
 
   grid_dep_wait();
   grid_dep_launch_dependents();
 
-  float v[8][8];
+  uint32_t w[kRows][Shape<S>::kWords] = {};
+  uint32_t xs = 127u;  // 8-bit x: lane i of the 16 that share rows holds row i's scale byte
+  if constexpr (S == Src::kQ8)
+    if (c < kRows && row0 + c < a.M)
+      xs = a.x_scale[(row0 + c) / a.x_scale_rows * a.ldx_scale + tk];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float scale = 1.f;
-    if (row0 + i < a.M) {
-      if constexpr (S == Src::kQ8)
-        scale = q8_scale(a.x_scale[(row0 + i) / a.x_scale_rows * a.ldx_scale + tk]);
-      load8<S>(a, row0 + i, col0, scale, v[i]);
-    } else {
+  for (int i = 0; i < kRows; ++i)
+    if (row0 + i < a.M) load8<S>(a, row0 + i, col0, w[i]);
+  if constexpr (S == Src::kQ8) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+    for (int i = 0; i < kRows; ++i) {
+      const float scale = q8_scale(__shfl_sync(0xFFFFFFFFu, xs, (lane & 16) + i));
+      const uint32_t lo = w[i][0], hi = w[i][1];
+      float v[8];
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        q8_unpack2((p < 2 ? lo : hi) >> (16 * (p & 1)), a.x_e5m2 != 0, v[2 * p], v[2 * p + 1]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[i][e] = __float_as_uint(v[e] * scale);
     }
   }
+  // elements 2p and 2p + 1 of row i
+  auto pair = [&](int i, int p) -> f2_t {
+    if constexpr (S == Src::kBf16)
+      return bf2_to_f2(w[i][p]);
+    else
+      return f2(__uint_as_float(w[i][2 * p]), __uint_as_float(w[i][2 * p + 1]));
+  };
+  // bit pattern of the largest magnitude of row i
+  auto row_max = [&](int i) -> uint32_t {
+    if constexpr (S == Src::kBf16) {
+      uint32_t m = __vmaxu2(__vmaxu2(w[i][0] & 0x7FFF7FFFu, w[i][1] & 0x7FFF7FFFu),
+                            __vmaxu2(w[i][2] & 0x7FFF7FFFu, w[i][3] & 0x7FFF7FFFu));
+      return max(m & 0xFFFF0000u, m << 16);
+    } else {
+      float m = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) m = max3_abs(m, __uint_as_float(w[i][e]), __uint_as_float(w[i][e + 1]));
+      return __float_as_uint(m);
+    }
+  };
 
-  uint32_t rsb[8];  // scale byte of each of this thread's rows
   uint32_t bsb = 0;
   if constexpr (BLOCK) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, abs_bits(v[i][e]));
+    for (int i = 0; i < kRows; ++i) m = max(m, row_max(i));
     m = lanes_max<32>(m);
-    if ((threadIdx.x & 31) == 0) wmax[warp][0] = m;
+    if (lane == 0) wmax[warp][0] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kQuantThreads / 32; ++w) m = max(m, wmax[w][0]);
+    for (int k = 0; k < kWarps; ++k) m = max(m, wmax[k][0]);
     bsb = q8_scale_byte<E5M2>(m);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) rsb[i] = bsb;
     if (threadIdx.x == 0) {
       if (a.q) a.q_scale[tm * a.ldq_scale + tk] = (uint8_t)bsb;
       if (a.qt) a.qt_scale[tk * a.ldqt_scale + tm] = (uint8_t)bsb;
     }
-  } else if (a.q) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, abs_bits(v[i][e]));
-      rsb[i] = q8_scale_byte<E5M2>(lanes_max<16>(m));
-      if (c == 0 && row0 + i < a.M) a.q_scale[(row0 + i) * a.ldq_scale + tk] = (uint8_t)rsb[i];
-    }
   }
   if (a.q) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kRows; ++i) {
+      uint32_t sb = bsb;
+      if constexpr (!BLOCK) {
+        sb = q8_scale_byte<E5M2>(lanes_max<16>(row_max(i)));
+        if (c == 0 && row0 + i < a.M) a.q_scale[(row0 + i) * a.ldq_scale + tk] = (uint8_t)sb;
+      }
       if (row0 + i >= a.M) continue;
-      const float inv = q8_inv_scale(rsb[i]);
+      const float inv = q8_inv_scale(sb);
+      const f2_t inv2 = f2(inv, inv);
+      float e[8];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) f2_split(f2_mul(pair(i, p), inv2), e[2 * p], e[2 * p + 1]);
       store8(a.q + (row0 + i) * a.ldq + col0,
-             make_uint2(q8_pack4<E5M2>(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv),
-                        q8_pack4<E5M2>(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv)),
-             a.K - col0);
+             make_uint2(q8_pack4<E5M2>(e[0], e[1], e[2], e[3]), q8_pack4<E5M2>(e[4], e[5], e[6], e[7])), a.K - col0);
     }
   }
   if (!a.qt) return;
 
   if constexpr (!BLOCK) {
+    // column maxima: this thread's rows, the warp's other row group, the warps
+    if constexpr (S == Src::kBf16) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t m = 0;
+      for (int p = 0; p < 4; ++p) {
+        uint32_t m = w[0][p] & 0x7FFF7FFFu;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i][e]));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));  // the warp's other row group
-      if ((threadIdx.x & 16) == 0) wmax[warp][8 * c + e] = m;
+        for (int i = 1; i < kRows; ++i) m = __vmaxu2(m, w[i][p] & 0x7FFF7FFFu);
+        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+        if (lane < 16) {
+          wmax[warp][8 * c + 2 * p] = m << 16;
+          wmax[warp][8 * c + 2 * p + 1] = m & 0xFFFF0000u;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float f = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRows; i += 2) f = max3_abs(f, __uint_as_float(w[i][e]), __uint_as_float(w[i + 1][e]));
+        uint32_t m = __float_as_uint(f);
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+        if (lane < 16) wmax[warp][8 * c + e] = m;
+      }
     }
     __syncthreads();
     if (threadIdx.x < kQ8Group) {
       uint32_t m = 0;
 #pragma unroll
-      for (int w = 0; w < kQuantThreads / 32; ++w) m = max(m, wmax[w][threadIdx.x]);
+      for (int k = 0; k < kWarps; ++k) m = max(m, wmax[k][threadIdx.x]);
       const uint32_t sb = q8_scale_byte<E5M2>(m);
-      cscale[threadIdx.x] = (uint8_t)sb;
+      cinv[threadIdx.x] = q8_inv_scale(sb);
       const int64_t col = tk * kQ8Group + threadIdx.x;
       if (col < a.K) a.qt_scale[col * a.ldqt_scale + tm] = (uint8_t)sb;
     }
     __syncthreads();
   }
+  const float binv = q8_inv_scale(bsb);
+  uint32_t* words = reinterpret_cast<uint32_t*>(tile);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float inv = q8_inv_scale(BLOCK ? bsb : (uint32_t)cscale[8 * c + e]);
-    tile[(8 * c + e) * 16 + (g ^ c)] =
-        make_uint2(q8_pack4<E5M2>(v[0][e] * inv, v[1][e] * inv, v[2][e] * inv, v[3][e] * inv),
-                   q8_pack4<E5M2>(v[4][e] * inv, v[5][e] * inv, v[6][e] * inv, v[7][e] * inv));
+  for (int p = 0; p < 4; ++p) {
+    const float2 ci = BLOCK ? make_float2(binv, binv) : *reinterpret_cast<const float2*>(&cinv[8 * c + 2 * p]);
+    const f2_t inv2 = f2(ci.x, ci.y);
+    float lo[kRows], hi[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) f2_split(f2_mul(pair(i, p), inv2), lo[i], hi[i]);
+    // 8-byte word r of column k (rows 8r..) at slot r ^ (k / 8)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float* f = h ? hi : lo;
+      const int k = 8 * c + 2 * p + h;
+      if constexpr (kRows == 8)
+        tile[k * 16 + (g ^ c)] = make_uint2(q8_pack4<E5M2>(f[0], f[1], f[2], f[3]), q8_pack4<E5M2>(f[4], f[5], f[6], f[7]));
+      else
+        words[(k * 16 + ((g >> 1) ^ c)) * 2 + (g & 1)] = q8_pack4<E5M2>(f[0], f[1], f[2], f[3]);
+    }
   }
   __syncthreads();
+  // 16 bytes a lane: words 2j and 2j + 1 of column k, swapped where k / 8 is odd
+  const int j = threadIdx.x & 7;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int k = g + 16 * i;  // column of the tile; lane c takes its rows 8c..
-    const int64_t col = tk * kQ8Group + k, row = tm * kQ8Group + 8 * c;
-    if (col < a.K && row < a.M)
-      store8(a.qt + col * a.ldqt + row, tile[k * 16 + (c ^ (k >> 3))], a.M - row);
+  for (int k = threadIdx.x >> 3; k < kQ8Group; k += kThreads / 8) {
+    const int64_t col = tk * kQ8Group + k, row = tm * kQ8Group + 16 * j;
+    const int kc = k >> 3;
+    uint4 u = reinterpret_cast<const uint4*>(tile)[k * 8 + (j ^ (kc >> 1))];
+    if (kc & 1) u = make_uint4(u.z, u.w, u.x, u.y);
+    if (col < a.K && row < a.M) store16(a.qt + col * a.ldqt + row, u, a.M - row);
   }
 }
 
@@ -202,7 +261,7 @@ cudaError_t launch_src(const QuantArgs& a, bool e5m2, bool block, unsigned grid,
   void (*k)(const QuantArgs) =
       e5m2 ? (block ? sp_quant_q8_kernel<S, true, true> : sp_quant_q8_kernel<S, true, false>)
            : (block ? sp_quant_q8_kernel<S, false, true> : sp_quant_q8_kernel<S, false, false>);
-  return pdl_launch(k, dim3(grid), dim3(kQuantThreads), 0, st, a);
+  return pdl_launch(k, dim3(grid), dim3(Shape<S>::kThreads), 0, st, a);
 }
 
 }  // namespace

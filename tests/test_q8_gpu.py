@@ -244,6 +244,21 @@ def test_matmul_exact_sums(M, N, K, af, bf, ablock, bblock):
     assert bool((out[M] == 7.5).all() and (out[:, 0] == 7.5).all() and (out[:, N + 1:] == 7.5).all())
 
 
+@pytest.mark.parametrize("M,N,K", [(1300, 2600, 200), (4000, 1500, 256), (2305, 4999, 129), (4096, 4104, 384),
+                                   (9000, 520, 1100)])
+def test_matmul_exact_sums_many_tiles(M, N, K):
+    """Several tiles per CTA or CTA pair, ragged on every side."""
+    g = gen(M + N)
+    a, sa, av = exact8(g, M, K, "e4m3", False)
+    b, sb, bv = exact8(g, N, K, "e4m3", True)
+    want = (av.to(DEV) @ bv.to(DEV).t()).cpu()
+    assert float(want.abs().max()) < 2.0 ** 24
+    assert same(ops.matmul_q8(a, sa, b, sb, out_dtype=F32), want)
+    assert same(ops.matmul_q8(a, sa, b, sb), want.float().to(BF16).double())
+    c = torch.ones(M, N, device=DEV)
+    assert same(ops.matmul_q8(a, sa, b, sb, out=c, accumulate=True), want + 1)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 256, 4096), (3, 72, 8192), (31, 130, 1000), (130, 300, 2048), (512, 384, 1024)])
 @pytest.mark.parametrize("af,block", [("e4m3", True), ("e5m2", False)])
 def test_matmul_real_values(M, N, K, af, block):
