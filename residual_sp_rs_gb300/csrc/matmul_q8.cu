@@ -245,9 +245,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---- tensor core instructions ------------------------------------------------
-    if (lane == 0 && leader) {
+    if (leader) {
+      const uint32_t one = elect_one();
       const uint32_t idesc = idesc_mxf8(SWAP ? a.b_e5m2 : a.a_e5m2, SWAP ? a.a_e5m2 : a.b_e5m2, kXRows * CG, p.BN);
       const uint32_t sfx = tmem + p.sf_col, sfy = sfx + 4;
+      // every lane waits, so that the warp stays together and agrees
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity, limit));
+        tmem_fence_after();
+        return ok;
+      };
       int s = 0, q = 0;
       uint32_t ph = 0, qph = 0;
       uint32_t n = 0;  // tiles of this CTA so far
@@ -256,50 +263,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d = tmem + (n & 1u ? p.acc1 : 0u);
         // the accumulators may overlap in the columns that the epilogue of
         // the tile before reads first; it has finished the tile before that
-        if (n > 0 && !mbar_wait_cluster(&sh.acc_free, (n - 1) & 1u, limit)) {
-          ok = false;
-          break;
-        }
-        tmem_fence_after();
+        if (n > 0 && !(ok = wait(&sh.acc_free, (n - 1) & 1u))) break;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (kb == kb0 || (kb & 3) == 0) {
-            if (!mbar_wait_cluster(&sh.sf_full[q], qph, limit)) {
-              ok = false;
-              break;
-            }
-            tmem_fence_after();
+            if (!(ok = wait(&sh.sf_full[q], qph))) break;
             const uint32_t src = sf_base + (uint32_t)q * sf_bytes;
-            tmem_cp_scales<CG>(sfx, desc_rows16(src));
-            for (uint32_t i = 0; i < scale_atoms_y(p.BN); ++i)
-              tmem_cp_scales<CG>(sfy + 4 * i, desc_rows16(src + kScaleAtom * (1 + i)));
-            umma_commit<CG>(&sh.sf_empty[q]);
+            tmem_cp_scales<CG>(sfx, desc_rows16(src), one);
+            tmem_cp_scales<CG>(sfy, desc_rows16(src + kScaleAtom), one);
+            if (p.BN > 128) tmem_cp_scales<CG>(sfy + 4, desc_rows16(src + 2 * kScaleAtom), one);
+            umma_commit<CG>(&sh.sf_empty[q], one);
             if (++q == kScaleSlots) {
               q = 0;
               qph ^= 1u;
             }
           }
-          if (!mbar_wait_cluster(&sh.full[s], ph, limit)) {
-            ok = false;
-            break;
-          }
-          tmem_fence_after();
+          if (!(ok = wait(&sh.full[s], ph))) break;
           const uint32_t st = base + (uint32_t)s * stage_bytes;
           const uint64_t dx = desc_sw128(st), dy = desc_sw128(st + kXBytes);
           const uint32_t id = idesc_scale_byte(idesc, (uint32_t)kb & 3u);
+          // 32 bytes of K a step (2 in the descriptors' units), the last block only as far as K goes
+          const uint32_t add = kb > kb0 ? 1u : 0u;
           const int64_t left = a.K - (int64_t)kb * 128;
-          const int steps = left >= 128 ? 4 : (int)((left + 31) >> 5);
-          for (int i = 0; i < steps; ++i)  // 32 bytes of K a step: 2 in the descriptor's units
-            umma_mxf8<CG>(d, dx + 2 * i, dy + 2 * i, id, sfx, sfy, kb > kb0 || i > 0);
-          umma_commit<CG>(&sh.empty[s]);
+          umma_mxf8<CG>(d, dx, dy, id, sfx, sfy, add, one);
+          if (left > 32) umma_mxf8<CG>(d, dx + 2, dy + 2, id, sfx, sfy, 1u, one);
+          if (left > 64) umma_mxf8<CG>(d, dx + 4, dy + 4, id, sfx, sfy, 1u, one);
+          if (left > 96) umma_mxf8<CG>(d, dx + 6, dy + 6, id, sfx, sfy, 1u, one);
+          umma_commit<CG>(&sh.empty[s], one);
           if (++s == p.stages) {
             s = 0;
             ph ^= 1u;
           }
         }
-        if (ok) umma_commit<CG>(&sh.acc_full);
+        if (ok) umma_commit<CG>(&sh.acc_full, one);
       }
-      if (!ok) report_status(a.status, kStatusMatmulWaitTimeout);
-      umma_commit<CG>(&sh.drain);
+      if (!ok && lane == 0) report_status(a.status, kStatusMatmulWaitTimeout);
+      umma_commit<CG>(&sh.drain, one);
       mbar_wait_cluster(&sh.drain, 0, limit);  // nothing in flight when tensor memory is freed
     }
   } else if (warp < 4) {
