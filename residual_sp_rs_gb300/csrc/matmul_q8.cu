@@ -53,6 +53,7 @@ struct MatmulPlan {
   int32_t stages;
   int32_t ks;            // CTAs that split K (CG = 1)
   int32_t xtiles, ytiles;
+  int32_t width;         // X tiles side by side in the order of the tiles
   int32_t nkb;           // 128-value blocks of K
   uint32_t tmem_cols;    // power of two
   uint32_t acc1;         // column of the second accumulator
@@ -69,10 +70,10 @@ struct Shared {
 
 __host__ __device__ constexpr uint32_t scale_atoms_y(int BN) { return (uint32_t)(BN + 127) / 128; }
 
-// Tile t of the list: columns of 16 X tiles, along Y within them, so that the
-// tiles in flight share their operands in L2.
-__device__ __forceinline__ void tile_at(const MatmulPlan& p, int64_t t, int CG, int64_t& tx, int64_t& ty) {
-  const int64_t w = 16 / CG, per = w * p.ytiles, g = t / per, in = t - g * per;
+// Tile t of the list: `width` tiles of X, along Y, then the next ones, so that
+// the tiles in flight share their operands in L2.
+__device__ __forceinline__ void tile_at(const MatmulPlan& p, int64_t t, int64_t& tx, int64_t& ty) {
+  const int64_t w = p.width, per = w * p.ytiles, g = t / per, in = t - g * per;
   const int64_t width = min(w, (int64_t)p.xtiles - g * w);
   tx = g * w + in % width;
   ty = in / width;
@@ -87,67 +88,48 @@ __device__ __forceinline__ void store_one(const MatmulArgs& a, int64_t o, float 
   }
 }
 
-// 32 columns y.. (ny of them inside C) of this warp's 32 rows x.., each lane
-// holding one row, to C: through 4 KB of shared memory (16-byte pieces, their
-// place in a row exclusive-or'ed with the row so that neither side meets a
-// bank conflict), from which neighbouring lanes write neighbouring addresses.
-__device__ __forceinline__ void store_rows(const MatmulArgs& a, unsigned char* buf, int64_t x, int64_t XR, int64_t y,
-                                           int ny, int lane, const uint32_t (&v)[32]) {
-  __syncwarp();  // the piece before this one has been read
-  if (a.c_f32) {
+// C goes out through 4 KB of shared memory per epilogue warp: 32 rows of 128
+// bytes (32 fp32 or 64 bf16 columns), the 16-byte pieces of a row exclusive-
+// or'ed with the row so that neither side meets a bank conflict, and from there
+// in whole 128-byte lines.
+__device__ __forceinline__ void stage_piece(unsigned char* buf, int lane, int q, uint4 v) {
+  *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) = v;
+}
+
+// Rows x.. of the staged piece to columns y.. of C, ny of them inside C.
+template <typename T>
+__device__ __forceinline__ void store_piece(const MatmulArgs& a, const unsigned char* buf, int64_t x, int64_t XR,
+                                            int64_t y, int ny, int lane) {
+  constexpr int kPer = 16 / sizeof(T);  // elements in 16 bytes
+  T* c = static_cast<T*>(a.c) + x * a.ldc + y;
+  const int rows = (int)min((int64_t)32, XR - x);
+  if (a.c_vec && ny % kPer == 0) {
+    const int q = lane & 7;
+    if (q * kPer >= ny) return;
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-          make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    __syncwarp();
-    float* c = static_cast<float*>(a.c) + x * a.ldc + y;
-    if (a.c_vec && ny == 32) {
-      const int q = lane & 7;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        if (x + r >= XR) continue;
-        float4 o = *reinterpret_cast<const float4*>(buf + r * 128 + ((q ^ (r & 7)) << 4));
-        float4* p = reinterpret_cast<float4*>(c + r * a.ldc + 4 * q);
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      if (r >= rows) break;
+      uint4 o = *reinterpret_cast<const uint4*>(buf + r * 128 + ((q ^ (r & 7)) << 4));
+      uint4* p = reinterpret_cast<uint4*>(c + r * a.ldc + kPer * q);
+      if constexpr (sizeof(T) == 4) {
         if (a.accumulate) {
-          const float4 b = *p;
-          o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
+          const float4 b = *reinterpret_cast<const float4*>(p);
+          o = make_uint4(__float_as_uint(__uint_as_float(o.x) + b.x), __float_as_uint(__uint_as_float(o.y) + b.y),
+                         __float_as_uint(__uint_as_float(o.z) + b.z), __float_as_uint(__uint_as_float(o.w) + b.w));
         }
-        *p = o;
       }
-    } else {
-      for (int r = 0; r < 32; ++r) {
-        if (x + r >= XR || lane >= ny) continue;
-        const float o = *reinterpret_cast<const float*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3));
-        float* p = c + r * a.ldc + lane;
-        *p = o + (a.accumulate ? *p : 0.f);
-      }
+      *p = o;
     }
   } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q + e]);
-      *reinterpret_cast<uint4*>(buf + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = Act16<__nv_bfloat16>::pack(f);
-    }
-    __syncwarp();
-    __nv_bfloat16* c = static_cast<__nv_bfloat16*>(a.c) + x * a.ldc + y;
-    if (a.c_vec && ny == 32) {
-      const int q = lane & 3;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2);
-        if (x + r < XR)
-          *reinterpret_cast<uint4*>(c + r * a.ldc + 8 * q) =
-              *reinterpret_cast<const uint4*>(buf + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+    for (int r = 0; r < rows; ++r)
+      for (int j = lane; j < ny; j += 32) {
+        T o = *reinterpret_cast<const T*>(buf + r * 128 + (((j / kPer) ^ (r & 7)) << 4) + sizeof(T) * (j % kPer));
+        T* p = c + r * a.ldc + j;
+        if constexpr (sizeof(T) == 4)
+          if (a.accumulate) o += *p;
+        *p = o;
       }
-    } else {
-      for (int r = 0; r < 32; ++r)
-        if (x + r < XR && lane < ny)
-          c[r * a.ldc + lane] = *reinterpret_cast<const __nv_bfloat16*>(
-              buf + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7));
-    }
   }
 }
 
@@ -213,11 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int64_t t = first; t < tiles && ok; t += step) {
         int64_t tx, ty;
-        tile_at(p, t, CG, tx, ty);
+        tile_at(p, t, tx, ty);
         const int32_t x0 = (int32_t)(tx * CG + (CG == 2 ? rank : 0)) * kXRows;
         const int32_t y0 = (int32_t)(ty * p.BN) + (CG == 2 ? (int32_t)rank * (p.BN / 2) : 0);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_cluster(&sh.empty[s], ph ^ 1u, limit)) {
+          if (!mbar_wait(&sh.empty[s], ph ^ 1u, limit)) {
             ok = false;
             break;
           }
@@ -241,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // leader's barriers count the pair's copies
       if (leader)
         for (int j = max(0, issued - p.stages); j < issued; ++j)
-          mbar_wait_cluster(&sh.full[j % p.stages], (uint32_t)(j / p.stages) & 1u, limit);
+          mbar_wait(&sh.full[j % p.stages], (uint32_t)(j / p.stages) & 1u, limit);
     }
   } else if (warp == 1) {
     // ---- tensor core instructions ------------------------------------------------
@@ -277,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               qph ^= 1u;
             }
           }
-          if (!(ok = wait(&sh.full[s], ph))) break;
+          if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.full[s], ph, limit)))) break;
           const uint32_t st = base + (uint32_t)s * stage_bytes;
           const uint64_t dx = desc_sw128(st), dy = desc_sw128(st + kXBytes);
           const uint32_t id = idesc_scale_byte(idesc, (uint32_t)kb & 3u);
@@ -313,17 +295,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int64_t t = first; t < tiles && ok; t += step) {
       int64_t tx, ty;
-      tile_at(p, t, CG, tx, ty);
+      tile_at(p, t, tx, ty);
       const int64_t x0 = (tx * CG + (CG == 2 ? rank : 0)) * kXRows, y0 = ty * p.BN;
+      uint4 w[6];  // the words of groups 4m .. 4m + 3 of rows tid, tid + 64, ... of X (128), then of Y
       for (int g = kb0 >> 2; g <= (kb1 - 1) >> 2 && kb0 < kb1; ++g) {
-        uint32_t w[6];
+        if (g == kb0 >> 2 || (g & 3) == 0) {
 #pragma unroll
-        for (int i = 0; i < 6; ++i) {  // rows tid, tid + 64, ... of X (128), then of Y
-          const int r = tid + 64 * i - (i < 2 ? 0 : kXRows);
-          const int64_t row = (i < 2 ? x0 : y0) + r;
-          w[i] = 0x7F7F7F7Fu;  // rows outside the tensor: zeros times one
-          if (i < 2 ? row < XR : r < p.BN && row < YR)
-            w[i] = __ldg(reinterpret_cast<const uint32_t*>(i < 2 ? xs + (row >> xshift) * xld : ys + (row >> yshift) * yld) + g);
+          for (int i = 0; i < 6; ++i) {
+            const int r = tid + 64 * i - (i < 2 ? 0 : kXRows);
+            const int64_t row = (i < 2 ? x0 : y0) + r;
+            w[i] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);  // rows outside: zeros times one
+            if (i < 2 ? row < XR : r < p.BN && row < YR)
+              w[i] = ld_cached((i < 2 ? xs + (row >> xshift) * xld : ys + (row >> yshift) * yld) + 16 * (g >> 2));
+          }
         }
         if (!mbar_wait_cluster(&sh.sf_empty[q], qph ^ 1u, limit)) {
           ok = false;
@@ -334,7 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 6; ++i) {
           const int r = tid + 64 * i;  // row r & 127 of atom r >> 7
           if (r < 128 * (1 + (int)scale_atoms_y(p.BN)))
-            *reinterpret_cast<uint32_t*>(dst + (r >> 7) * kScaleAtom + (r & 31) * 16 + ((r & 127) >> 5) * 4) = w[i];
+            *reinterpret_cast<uint32_t*>(dst + (r >> 7) * kScaleAtom + (r & 31) * 16 + ((r & 127) >> 5) * 4) =
+                (g & 2) ? ((g & 1) ? w[i].w : w[i].z) : ((g & 1) ? w[i].y : w[i].x);
         }
         fence_async_shared();
         __syncwarp();
@@ -359,30 +344,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int64_t t = first; t < tiles; t += step, ++n) {
       int64_t tx, ty;
-      tile_at(p, t, CG, tx, ty);
+      tile_at(p, t, tx, ty);
       const int64_t x = (tx * CG + (CG == 2 ? rank : 0)) * kXRows + 32 * w4 + lane, y0 = ty * p.BN;
       const uint32_t acc = tmem + (n & 1u ? p.acc1 : 0u) + ((uint32_t)(32 * w4) << 16);
       if (kb0 < kb1 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&sh.acc_full, n & 1u, limit));
       if (!ok && lane == 0 && w4 == 0) report_status(a.status, kStatusMatmulWaitTimeout);
       tmem_fence_after();
-      const int chunks = (p.BN + 31) / 32;
+      // columns a chunk: 128 bytes of a row of C, the columns that the
+      // accumulators may share first
+      const int width = SWAP || a.c_f32 ? 32 : 64, chunks = (p.BN + width - 1) / width;
       for (int c = 0; c < chunks; ++c) {
-        // the columns that the accumulators may share come first
-        const int col = 32 * (n & 1u ? c : chunks - 1 - c);
-        uint32_t v[32];
-        if (kb0 < kb1 && ok) {
-          if (p.BN - col >= 32) {
-            tmem_ld32(acc + col, v);
+        const int col0 = width * (n & 1u ? c : chunks - 1 - c);
+        if (!SWAP) __syncwarp();  // the staged piece before this one has been read
+        for (int col = col0; col < min(col0 + width, p.BN); col += 32) {
+          uint32_t v[32];
+          if (kb0 < kb1 && ok) {
+            if (p.BN - col >= 32) {
+              tmem_ld32(acc + col, v);
+            } else {
+              uint32_t u[16];
+              tmem_ld16(acc + col, u);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = u[i];
+            }
+            tmem_ld_wait();
           } else {
-            uint32_t u[16];
-            tmem_ld16(acc + col, u);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = u[i];
+            for (int i = 0; i < 32; ++i) v[i] = ok ? 0u : 0x7FC00000u;
           }
-          tmem_ld_wait();
-        } else {
+          if constexpr (SWAP) {
+            const int ny = (int)min((int64_t)min(32, p.BN - col), YR - (y0 + col));  // columns inside C
+            if (p.ks > 1) {
+              float* part = reinterpret_cast<float*>(dsm) + col * kXRows + 32 * w4 + lane;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = ok ? 0u : 0x7FC00000u;
+              for (int i = 0; i < 32; ++i)
+                if (i < ny) part[i * kXRows] = __uint_as_float(v[i]);
+            } else if (x < XR) {
+              // a lane's columns are rows of C: 32 lanes write neighbouring elements
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < ny) store_one(a, (y0 + col + i) * a.ldc + x, __uint_as_float(v[i]));
+            }
+          } else if (a.c_f32) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              stage_piece(stage_c, lane, q, make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float f[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q + e]);
+              stage_piece(stage_c, lane, q + (col - col0) / 8, Act16<__nv_bfloat16>::pack(f));
+            }
+          }
         }
         if (c == 0) {
           tmem_fence_before();
@@ -394,22 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive(&sh.acc_free);
           }
         }
-        const int64_t y = y0 + col;
-        const int ny = (int)min((int64_t)min(32, p.BN - col), YR - y);  // columns inside C
-        if (p.ks > 1) {
-          float* part = reinterpret_cast<float*>(dsm) + col * kXRows + 32 * w4 + lane;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < ny) part[i * kXRows] = __uint_as_float(v[i]);
-        } else if constexpr (SWAP) {
-          // a lane's columns are rows of C: 32 lanes write neighbouring elements
-          if (x < XR) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < ny) store_one(a, (y + i) * a.ldc + x, __uint_as_float(v[i]));
-          }
-        } else if (ny > 0) {
-          store_rows(a, stage_c, x - lane, XR, y, ny, lane, v);
+        if constexpr (!SWAP) {
+          __syncwarp();
+          const int ny = (int)min((int64_t)min(width, p.BN - col0), YR - (y0 + col0));
+          if (a.c_f32)
+            store_piece<float>(a, stage_c, x - lane, XR, y0 + col0, ny, lane);
+          else
+            store_piece<__nv_bfloat16>(a, stage_c, x - lane, XR, y0 + col0, ny, lane);
         }
       }
     }
@@ -424,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();  // one tile per cluster: every CTA's part is in its shared memory
     if constexpr (SWAP) {
       int64_t tx, ty;
-      tile_at(p, first, CG, tx, ty);
+      tile_at(p, first, tx, ty);
       const int l = threadIdx.x & 127;
       const int64_t x = tx * kXRows + l;
       const int cols = (int)min((int64_t)p.BN, YR - ty * p.BN);
@@ -527,6 +533,7 @@ Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
   }
   MatmulPlan& p = *best;
   p.nkb = (int32_t)nkb;
+  p.width = 16 / ch.cg;
   const uint32_t sf_cols = 16;  // 4 for X and 4 or 8 for Y; every start a multiple of 16
   p.tmem_cols = pow2_at_least((p.ks > 1 ? p.BN : 2 * p.BN) + sf_cols);
   if (p.tmem_cols > 512) p.tmem_cols = 512;
