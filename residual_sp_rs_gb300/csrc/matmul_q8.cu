@@ -17,7 +17,7 @@
 //   warp 1     issues the tensor core instructions (and owns tensor memory)
 //   warps 2-3  bring the scale bytes: per 4 blocks of K one 32-bit word per
 //              row, into the 32 x 16 byte layout that goes to tensor memory
-//   warps 4-7  epilogue: tensor memory to C
+//   warps 4-   epilogue: tensor memory to C
 // Tiles are dealt to the resident CTAs in turn; the two accumulators in tensor
 // memory let the epilogue of one tile run under the products of the next.
 // Few tiles (decoding): `ks` CTAs of a cluster split K and add their fp32
@@ -40,7 +40,10 @@ namespace spf {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Two epilogue warps per quarter of the lanes where a tile of C is wide; a short
+// side has one, and two CTAs of it fit on an SM.
+__host__ __device__ constexpr int epilogue_warps(bool swap) { return swap ? 4 : 8; }
+__host__ __device__ constexpr int threads(bool swap) { return 128 + 32 * epilogue_warps(swap); }
 constexpr int kXRows = 128;                   // rows of X per CTA
 constexpr uint32_t kXBytes = kXRows * 128;    // one stage of X
 constexpr int kMaxStages = 12;
@@ -134,7 +137,7 @@ __device__ __forceinline__ void store_piece(const MatmulArgs& a, const unsigned 
 }
 
 template <int CG, bool SWAP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
     sp_matmul_q8_kernel(const MatmulArgs a, const MatmulPlan p, const __grid_constant__ CUtensorMap mapx,
                         const __grid_constant__ CUtensorMap mapy) {
   extern __shared__ __align__(1024) unsigned char dsm_raw[];
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.sf_empty[s], 1);
     }
     mbar_init(&sh.acc_full, 1);
-    mbar_init(&sh.acc_free, 4 * CG);
+    mbar_init(&sh.acc_free, epilogue_warps(SWAP) * CG);
     mbar_init(&sh.drain, 1);
     fence_mbar_init();
   }
@@ -246,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the accumulators may overlap in the columns that the epilogue of
         // the tile before reads first; it has finished the tile before that
         if (n > 0 && !(ok = wait(&sh.acc_free, (n - 1) & 1u))) break;
+        bool landed = false;  // this stage's data, tested for while the products before it were issued
         for (int kb = kb0; kb < kb1; ++kb) {
           if (kb == kb0 || (kb & 3) == 0) {
             if (!(ok = wait(&sh.sf_full[q], qph))) break;
@@ -259,10 +263,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               qph ^= 1u;
             }
           }
-          if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.full[s], ph, limit)))) break;
+          if (!__all_sync(0xFFFFFFFFu, landed) &&
+              !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.full[s], ph, limit))))
+            break;
           const uint32_t st = base + (uint32_t)s * stage_bytes;
           const uint64_t dx = desc_sw128(st), dy = desc_sw128(st + kXBytes);
           const uint32_t id = idesc_scale_byte(idesc, (uint32_t)kb & 3u);
+          uint64_t* const done = &sh.empty[s];
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1u;
+          }
+          landed = mbar_test(&sh.full[s], ph);
           // 32 bytes of K a step (2 in the descriptors' units), the last block only as far as K goes
           const uint32_t add = kb > kb0 ? 1u : 0u;
           const int64_t left = a.K - (int64_t)kb * 128;
@@ -270,11 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (left > 32) umma_mxf8<CG>(d, dx + 2, dy + 2, id, sfx, sfy, 1u, one);
           if (left > 64) umma_mxf8<CG>(d, dx + 4, dy + 4, id, sfx, sfy, 1u, one);
           if (left > 96) umma_mxf8<CG>(d, dx + 6, dy + 6, id, sfx, sfy, 1u, one);
-          umma_commit<CG>(&sh.empty[s], one);
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1u;
-          }
+          umma_commit<CG>(done, one);
         }
         if (ok) umma_commit<CG>(&sh.acc_full, one);
       }
@@ -338,8 +346,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && tid == 0) report_status(a.status, kStatusMatmulWaitTimeout);
   } else {
     // ---- epilogue -----------------------------------------------------------------
-    const int w4 = warp & 3;
-    unsigned char* stage_c = dsm + (uint32_t)p.stages * stage_bytes + kScaleSlots * sf_bytes + w4 * kStoreBytes;
+    const int w4 = warp & 3, half = (warp - 4) >> 2, halves = epilogue_warps(SWAP) / 4;
+    unsigned char* stage_c = dsm + (uint32_t)p.stages * stage_bytes + kScaleSlots * sf_bytes + (warp - 4) * kStoreBytes;
+    // this warp has read its first columns of the tile (and every one of the
+    // tile before)
+    auto free_acc = [&]() {
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          mbar_arrive_cluster(map_cta(smem_addr(&sh.acc_free), 0));
+        else
+          mbar_arrive(&sh.acc_free);
+      }
+    };
     uint32_t n = 0;
     bool ok = true;
     for (int64_t t = first; t < tiles; t += step, ++n) {
@@ -353,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // columns a chunk: 128 bytes of a row of C, the columns that the
       // accumulators may share first
       const int width = SWAP || a.c_f32 ? 32 : 64, chunks = (p.BN + width - 1) / width;
-      for (int c = 0; c < chunks; ++c) {
+      if (half >= chunks) free_acc();  // nothing to read for this warp
+      for (int c = half; c < chunks; c += halves) {
         const int col0 = width * (n & 1u ? c : chunks - 1 - c);
         if (!SWAP) __syncwarp();  // the staged piece before this one has been read
         for (int col = col0; col < min(col0 + width, p.BN); col += 32) {
@@ -399,16 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (c == 0) {
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CG == 2)
-              mbar_arrive_cluster(map_cta(smem_addr(&sh.acc_free), 0));
-            else
-              mbar_arrive(&sh.acc_free);
-          }
-        }
+        if (c == half) free_acc();
         if constexpr (!SWAP) {
           __syncwarp();
           const int ny = (int)min((int64_t)min(width, p.BN - col0), YR - (y0 + col0));
@@ -434,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int l = threadIdx.x & 127;
       const int64_t x = tx * kXRows + l;
       const int cols = (int)min((int64_t)p.BN, YR - ty * p.BN);
-      for (int col = (int)rank + p.ks * (threadIdx.x >> 7); col < cols; col += 2 * p.ks) {
+      for (int col = (int)rank + p.ks * (threadIdx.x >> 7); col < cols; col += threads(SWAP) / 128 * p.ks) {
         float sum = 0.f;
         for (int r = 0; r < p.ks; ++r) sum += ld_cluster_f32(map_cta(base + (uint32_t)(col * kXRows + l) * 4u, r));
         if (x < XR) store_one(a, (ty * p.BN + col) * a.ldc + x, sum);
@@ -493,17 +505,28 @@ struct Choice {
   bool swap;
 };
 
+constexpr int kShortSide = 64;
+
 int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
-// Tile shape and split of K: the least of an estimate of the time, in clocks.
-// A block of K costs a CTA the larger of its products (2 BN clocks for 128 x
-// BN x 128) and its loads (its rows of 128 bytes at about kLoadRate a clock);
-// a CTA works off its share of the tiles one after the other, and pays once for
-// starting, for the last tile's epilogue and, with K split, for the join.
+// Tile shape and split of K: the least of an estimate of the time, in clocks,
+// whose constants are measured (back to back on one GB300 at about 2 GHz):
+//   a block of K costs a CTA the largest of its products (2 BN clocks for 128
+//   x BN x 128), its loads (56 bytes a clock from L2 to an SM: 128 x 256 tiles
+//   0.46, pairs 0.35, 128 x 128 tiles 0.28 us a block) and the issue of its
+//   instructions (0.22 us whatever BN is);
+//   starting and ending a kernel 2.6 us, the last tile's epilogue 19 clocks a
+//   column (90 with the operands swapped, whose stores are narrow), a pair's
+//   cluster barriers and the turns of its tiles more than a single CTA's
+//   (4096 x 1536 x 768 in 192 columns: 9.4 us single, 11.4 us paired; 16384 x
+//   4096 x 8192 in 256 columns: 333 and 291 us);
+//   nothing is faster than its bytes from memory.
 Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
-  constexpr double kLoadRate = 55.0, kStart = 2500.0, kPerColumn = 12.0, kJoin = 1500.0;
+  constexpr double kLoadRate = 56.0, kIssue = 430.0, kStart = 5200.0, kColumn = 19.0, kSwapColumn = 90.0, kJoin = 1500.0;
+  constexpr double kPair = 2000.0, kPairTurn = 2500.0, kMemoryRate = 3300.0;
   Choice ch = {1, false};
   double least = 1e300;
+  const double memory = ((double)(a.M + a.N) * a.K + (double)a.M * a.N * (a.c_f32 ? 4 : 2)) / kMemoryRate;
   const int64_t nkb = ceil_div(a.K, 128);
   for (int mode = 0; mode < 3; ++mode) {  // one CTA, a pair of CTAs, one CTA with the operands swapped
     const int cg = mode == 1 ? 2 : 1;
@@ -515,11 +538,15 @@ Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
       const int64_t xt = ceil_div(XR, (int64_t)kXRows * cg), yt = ceil_div(YR, BN);
       for (int ks = 1; ks <= 8; ks *= 2) {
         // of clusters of 2, 4 and 8 CTAs 152, 144 and 120 CTAs are resident at once on 152 SMs
-        const int64_t room = ks == 8 ? sms * 15 / 19 : ks == 4 ? sms * 18 / 19 : sms;
+        const int per_sm = swap && BN <= kShortSide ? 2 : 1;
+        const int64_t room = per_sm * (ks == 8 ? sms * 15 / 19 : ks == 4 ? sms * 18 / 19 : sms);
         if (ks > 1 && (!swap || ks > nkb || xt * yt * ks > room)) break;
-        const double block = fmax(2.0 * BN, (kXRows + BN / cg) * 128 / kLoadRate);
-        const int64_t turns = ceil_div(xt * yt * ks * cg, sms / cg * cg);
-        const double t = kStart + (double)turns * ceil_div(nkb, ks) * block + kPerColumn * BN + (ks > 1 ? kJoin : 0.0);
+        const int64_t ctas = xt * yt * ks * cg;
+        const int64_t turns = ceil_div(ctas, per_sm * sms / cg * cg);
+        const double load = (kXRows + BN / cg) * 128 / kLoadRate * (ctas > sms ? per_sm : 1);
+        const double path = (double)turns * (ceil_div(nkb, ks) * fmax(fmax(2.0 * BN, load), kIssue) + (cg == 2 ? kPairTurn : 0.0));
+        const double t = kStart + fmax(path, memory) + 0.1 * path + (swap ? kSwapColumn : kColumn) * BN +
+                         (cg == 2 ? kPair : 0.0) + (ks > 1 ? kJoin : 0.0);
         if (t < least) {
           least = t;
           ch = {cg, swap};
@@ -540,8 +567,12 @@ Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
   p.sf_col = p.tmem_cols - sf_cols;
   p.acc1 = p.sf_col - p.BN;  // overlaps the first accumulator by less than 32 columns
   const uint32_t stage = kXBytes + (uint32_t)(p.BN / ch.cg) * 128u;
-  const uint32_t rest = 1024 + kScaleSlots * kScaleAtom * (1 + scale_atoms_y(p.BN)) + (ch.swap ? 0 : 4 * kStoreBytes);
-  int64_t stages = ((int64_t)optin - 1024 - rest) / stage;  // 1024: the kernel's static shared memory, rounded up
+  const uint32_t rest = 1024 + kScaleSlots * kScaleAtom * (1 + scale_atoms_y(p.BN)) + (ch.swap ? 0 : epilogue_warps(false) * kStoreBytes);
+  // 2048: the kernel's static shared memory and the driver's, rounded up.  A short side
+  // leaves half of an SM's shared memory to a second CTA: the split's, or the
+  // next kernel's, which then starts under this one's end.
+  const int64_t budget = (ch.swap && p.BN <= kShortSide ? optin / 2 : optin) - 2048;
+  int64_t stages = (budget - rest) / stage;
   if (stages > kMaxStages) stages = kMaxStages;
   const int64_t need = ceil_div(nkb, p.ks) * ceil_div((int64_t)p.xtiles * p.ytiles * p.ks * ch.cg, sms);
   // no more than the CTA ever fills, but room for the join's fp32 sums
@@ -568,7 +599,7 @@ cudaError_t launch(const MatmulArgs& a, MatmulPlan p, int sms, cudaStream_t st) 
   const int group = CG * p.ks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.ks > 1 ? tiles : min(tiles, (int64_t)(sms / CG))) * group));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads(SWAP));
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
