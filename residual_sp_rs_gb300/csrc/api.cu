@@ -509,6 +509,7 @@ sp_status_t sp_quantize_q8(const sp_quantize_q8_desc_t* d, const void* x, const 
   a.ldq_scale = d->ldq_scale;
   a.ldqt_scale = d->ldqt_scale;
   a.ktiles = kg;
+  a.tiles = mg * kg;
   a.x_scale_rows = d->x_scale_rows;
   a.x_e5m2 = d->x_dtype == SP_ELEM_E5M2;
   a.vec = aligned(x, 16) && d->ldx * xb % 16 == 0;

@@ -2,6 +2,7 @@
 // libspfuse (not part of the C ABI).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -117,6 +118,10 @@ cudaError_t launch_fwd_tma_rms_q8(const FwdArgs& a, int T, const FwdTmaPlan& p, 
 cudaError_t launch_fwd_tma_ln_q8(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid, cudaStream_t st);
 cudaError_t launch_fwd_tma_rms_ch_q8(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid, cudaStream_t st);
 cudaError_t launch_fwd_tma_ln_ch_q8(const FwdArgs& a, int T, const FwdTmaPlan& p, dim3 grid, cudaStream_t st);
+
+// Tensor map of [rows, K] bytes, `ld` apart, in boxes of 128 bytes x `box`
+// rows, with the 128-byte swizzle or none.
+cudaError_t byte_map(const void* p, int64_t rows, int64_t K, int64_t ld, int box, bool swizzle, CUtensorMap* map);
 
 // x_dtype: sp_elem_t; the rest of the shape is in the arguments.
 cudaError_t launch_quant_q8(const QuantArgs& a, int x_dtype, bool e5m2, bool block, cudaStream_t st);

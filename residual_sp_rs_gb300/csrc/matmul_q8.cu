@@ -481,18 +481,21 @@ cudaError_t encode_tiled(EncodeTiled* out) {
   return cudaSuccess;
 }
 
-// [rows, K] bytes, `ld` apart, in boxes of 128 bytes x `box` rows.
-cudaError_t operand_map(const void* p, int64_t rows, int64_t K, int64_t ld, int box, CUtensorMap* map) {
+}  // namespace
+
+cudaError_t byte_map(const void* p, int64_t rows, int64_t K, int64_t ld, int box, bool swizzle, CUtensorMap* map) {
   EncodeTiled encode;
   const cudaError_t e = encode_tiled(&encode);
   if (e != cudaSuccess) return e;
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
   const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, ones[2] = {1, 1};
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, boxes, ones,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+namespace {
 
 uint32_t pow2_at_least(uint32_t n) {
   uint32_t c = 32;
@@ -588,8 +591,8 @@ cudaError_t launch(const MatmulArgs& a, MatmulPlan p, int sms, cudaStream_t st) 
   CUtensorMap mx = {}, my = {};
   if (p.nkb > 0) {
     const int64_t XR = SWAP ? a.N : a.M, YR = SWAP ? a.M : a.N;
-    cudaError_t e = operand_map(SWAP ? a.b : a.a, XR, a.K, SWAP ? a.ldb : a.lda, kXRows, &mx);
-    if (e == cudaSuccess) e = operand_map(SWAP ? a.a : a.b, YR, a.K, SWAP ? a.lda : a.ldb, p.BN / CG, &my);
+    cudaError_t e = byte_map(SWAP ? a.b : a.a, XR, a.K, SWAP ? a.ldb : a.lda, kXRows, true, &mx);
+    if (e == cudaSuccess) e = byte_map(SWAP ? a.a : a.b, YR, a.K, SWAP ? a.lda : a.ldb, p.BN / CG, true, &my);
     if (e != cudaSuccess) return e;
   }
   auto k = sp_matmul_q8_kernel<CG, SWAP>;

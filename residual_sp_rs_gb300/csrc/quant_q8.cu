@@ -14,19 +14,27 @@
 // form one word of the transposed tile.  That tile goes through shared memory
 // (8-byte word r of column k at slot r ^ (k / 8), so that neither side meets a
 // bank conflict) and leaves 128 bytes of a column at a time.
+//
+// An 8-bit tile is 16 KB, too little for the resident CTAs to keep the memory
+// busy between their barriers.  So two CTAs stay on each SM, and tiled bulk
+// copies bring the next kRing tiles of each while one is worked on.
 #include "common.cuh"
 #include "launch.h"
 #include "q8.cuh"
+#include "umma.cuh"
 
 namespace spf {
 
 namespace {
 
+constexpr int kRing = 3;                    // 8-bit input: tiles in flight per CTA
+constexpr uint32_t kTileBytes = 128 * 128;
+
 enum class Src { kF32, kBf16, kQ8 };
 
 template <Src S>
 struct Shape {
-  static constexpr int kBytes = S == Src::kF32 ? 4 : S == Src::kBf16 ? 2 : 1;
+  static constexpr int kBytes = S == Src::kF32 ? 4 : 2;      // of an element (not asked for 8-bit input)
   static constexpr int kRows = S == Src::kBf16 ? 8 : 4;      // rows per thread
   static constexpr int kThreads = 16 * kQ8Group / kRows;
   static constexpr int kWords = S == Src::kBf16 ? 4 : 8;     // registers per row
@@ -39,25 +47,18 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   return r;
 }
 
-// Eight consecutive elements of a row from column `col` on, zero past K: the
-// raw words, for an 8-bit x the 8 bytes in w[0..1].
+// Eight consecutive elements of a row from column `col` on, zero past K.
 template <Src S>
 __device__ __forceinline__ void load8(const QuantArgs& a, int64_t row, int64_t col, uint32_t (&w)[Shape<S>::kWords]) {
   const char* p = static_cast<const char*>(a.x) + (row * a.ldx + col) * Shape<S>::kBytes;
   if (a.vec && col + 8 <= a.K) {
-    if constexpr (S == Src::kQ8) {
-      const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
-      w[0] = u.x;
-      w[1] = u.y;
-    } else {
 #pragma unroll
-      for (int i = 0; i < Shape<S>::kBytes / 2; ++i) {
-        const uint4 u = ld_stream(p + 16 * i);
-        w[4 * i] = u.x;
-        w[4 * i + 1] = u.y;
-        w[4 * i + 2] = u.z;
-        w[4 * i + 3] = u.w;
-      }
+    for (int i = 0; i < Shape<S>::kBytes / 2; ++i) {
+      const uint4 u = ld_stream(p + 16 * i);
+      w[4 * i] = u.x;
+      w[4 * i + 1] = u.y;
+      w[4 * i + 2] = u.z;
+      w[4 * i + 3] = u.w;
     }
     return;
   }
@@ -68,10 +69,8 @@ __device__ __forceinline__ void load8(const QuantArgs& a, int64_t row, int64_t c
     if (col + e >= a.K) continue;
     if constexpr (S == Src::kF32)
       w[e] = *(reinterpret_cast<const uint32_t*>(p) + e);
-    else if constexpr (S == Src::kBf16)
-      w[e / 2] |= (uint32_t) * (reinterpret_cast<const uint16_t*>(p) + e) << (16 * (e & 1));
     else
-      w[e / 4] |= (uint32_t) * (reinterpret_cast<const uint8_t*>(p) + e) << (8 * (e & 3));
+      w[e / 2] |= (uint32_t) * (reinterpret_cast<const uint16_t*>(p) + e) << (16 * (e & 1));
   }
 }
 
@@ -95,183 +94,236 @@ __device__ __forceinline__ void store16(uint8_t* p, uint4 w, int64_t n) {
 }
 
 template <Src S, bool E5M2, bool BLOCK>
-__global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads) sp_quant_q8_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads) sp_quant_q8_kernel(const QuantArgs a, const __grid_constant__ CUtensorMap map) {
   constexpr int kRows = Shape<S>::kRows, kThreads = Shape<S>::kThreads, kWarps = kThreads / 32;
   __shared__ uint32_t wmax[kWarps][kQ8Group];          // column maxima of each warp
   __shared__ float cinv[kQ8Group];                     // 2^-s of each column
   __shared__ __align__(16) uint2 tile[kQ8Group * 16];  // transposed bytes
 
   const int c = threadIdx.x & 15, g = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tm = blockIdx.x / a.ktiles, tk = blockIdx.x - tm * a.ktiles;
-  const int64_t row0 = tm * kQ8Group + kRows * g, col0 = tk * kQ8Group + 8 * c;
-
+  extern __shared__ __align__(128) unsigned char ring_raw[];
+  unsigned char* const ring = ring_raw + ((128u - (smem_addr(ring_raw) & 127u)) & 127u);
+  __shared__ uint64_t landed[kRing];
+  if constexpr (S == Src::kQ8) {
+    if (threadIdx.x == 0) {
+      prefetch_tensor_map(&map);
+      for (int s = 0; s < kRing; ++s) mbar_init(&landed[s], 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
   grid_dep_wait();
   grid_dep_launch_dependents();
 
-  uint32_t w[kRows][Shape<S>::kWords] = {};
-  uint32_t xs = 127u;  // 8-bit x: lane i of the 16 that share rows holds row i's scale byte
+  // 8-bit x: tile `t` to stage `s` of the ring
+  auto fetch = [&](int64_t t, int s) {
+    if (t >= a.tiles) return;
+    mbar_arrive_expect_tx(&landed[s], kTileBytes);
+    tma_load_2d<1>(smem_addr(ring) + s * kTileBytes, &map, (int32_t)(t % a.ktiles * kQ8Group),
+                   (int32_t)(t / a.ktiles * kQ8Group), smem_addr(&landed[s]));
+  };
   if constexpr (S == Src::kQ8)
-    if (c < kRows && row0 + c < a.M)
-      xs = a.x_scale[(row0 + c) / a.x_scale_rows * a.ldx_scale + tk];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    if (row0 + i < a.M) load8<S>(a, row0 + i, col0, w[i]);
-  if constexpr (S == Src::kQ8) {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float scale = q8_scale(__shfl_sync(0xFFFFFFFFu, xs, (lane & 16) + i));
-      const uint32_t lo = w[i][0], hi = w[i][1];
-      float v[8];
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-        q8_unpack2((p < 2 ? lo : hi) >> (16 * (p & 1)), a.x_e5m2 != 0, v[2 * p], v[2 * p + 1]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[i][e] = __float_as_uint(v[e] * scale);
-    }
-  }
-  // elements 2p and 2p + 1 of row i
-  auto pair = [&](int i, int p) -> f2_t {
-    if constexpr (S == Src::kBf16)
-      return bf2_to_f2(w[i][p]);
-    else
-      return f2(__uint_as_float(w[i][2 * p]), __uint_as_float(w[i][2 * p + 1]));
-  };
-  // bit pattern of the largest magnitude of row i
-  auto row_max = [&](int i) -> uint32_t {
-    if constexpr (S == Src::kBf16) {
-      uint32_t m = __vmaxu2(__vmaxu2(w[i][0] & 0x7FFF7FFFu, w[i][1] & 0x7FFF7FFFu),
-                            __vmaxu2(w[i][2] & 0x7FFF7FFFu, w[i][3] & 0x7FFF7FFFu));
-      return max(m & 0xFFFF0000u, m << 16);
-    } else {
-      float m = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) m = max3_abs(m, __uint_as_float(w[i][e]), __uint_as_float(w[i][e + 1]));
-      return __float_as_uint(m);
-    }
-  };
+    if (threadIdx.x == 0)
+      for (int s = 0; s < kRing; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  int stage = 0;
+  uint32_t phase = 0;
 
-  uint32_t bsb = 0;
-  if constexpr (BLOCK) {
-    uint32_t m = 0;
+  for (int64_t t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+    const int64_t tm = t / a.ktiles, tk = t - tm * a.ktiles;
+    const int64_t row0 = tm * kQ8Group + kRows * g, col0 = tk * kQ8Group + 8 * c;
+    uint32_t w[kRows][Shape<S>::kWords] = {};
+    uint32_t xs = 127u;  // 8-bit x: lane i of the 16 that share rows holds row i's scale byte
+    if constexpr (S == Src::kQ8)
+      if (c < kRows && row0 + c < a.M)
+        xs = a.x_scale[(row0 + c) / a.x_scale_rows * a.ldx_scale + tk];
+    if constexpr (S == Src::kQ8) {
+      const bool ok = mbar_wait(&landed[stage], phase, kWaitNs);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) m = max(m, row_max(i));
-    m = lanes_max<32>(m);
-    if (lane == 0) wmax[warp][0] = m;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) m = max(m, wmax[k][0]);
-    bsb = q8_scale_byte<E5M2>(m);
-    if (threadIdx.x == 0) {
-      if (a.q) a.q_scale[tm * a.ldq_scale + tk] = (uint8_t)bsb;
-      if (a.qt) a.qt_scale[tk * a.ldqt_scale + tm] = (uint8_t)bsb;
-    }
-  }
-  if (a.q) {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      uint32_t sb = bsb;
-      if constexpr (!BLOCK) {
-        sb = q8_scale_byte<E5M2>(lanes_max<16>(row_max(i)));
-        if (c == 0 && row0 + i < a.M) a.q_scale[(row0 + i) * a.ldq_scale + tk] = (uint8_t)sb;
+      for (int i = 0; i < kRows; ++i) {  // what never landed goes on as NaN
+        const uint2 u = *reinterpret_cast<const uint2*>(ring + stage * kTileBytes + (kRows * g + i) * 128 + 8 * c);
+        w[i][0] = ok ? u.x : 0x7F7F7F7Fu;
+        w[i][1] = ok ? u.y : 0x7F7F7F7Fu;
       }
-      if (row0 + i >= a.M) continue;
-      const float inv = q8_inv_scale(sb);
-      const f2_t inv2 = f2(inv, inv);
-      float e[8];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) f2_split(f2_mul(pair(i, p), inv2), e[2 * p], e[2 * p + 1]);
-      store8(a.q + (row0 + i) * a.ldq + col0,
-             make_uint2(q8_pack4<E5M2>(e[0], e[1], e[2], e[3]), q8_pack4<E5M2>(e[4], e[5], e[6], e[7])), a.K - col0);
-    }
-  }
-  if (!a.qt) return;
-
-  if constexpr (!BLOCK) {
-    // column maxima: this thread's rows, the warp's other row group, the warps
-    if constexpr (S == Src::kBf16) {
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        uint32_t m = w[0][p] & 0x7FFF7FFFu;
-#pragma unroll
-        for (int i = 1; i < kRows; ++i) m = __vmaxu2(m, w[i][p] & 0x7FFF7FFFu);
-        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-        if (lane < 16) {
-          wmax[warp][8 * c + 2 * p] = m << 16;
-          wmax[warp][8 * c + 2 * p + 1] = m & 0xFFFF0000u;
-        }
+      __syncthreads();  // the stage, and the last tile's words and maxima, have been read
+      if (threadIdx.x == 0) fetch(t + (int64_t)kRing * gridDim.x, stage);
+      if (++stage == kRing) {
+        stage = 0;
+        phase ^= 1u;
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float f = 0.f;
+      for (int i = 0; i < kRows; ++i)
+        if (row0 + i < a.M) load8<S>(a, row0 + i, col0, w[i]);
+    }
+    if constexpr (S == Src::kQ8) {
 #pragma unroll
-        for (int i = 0; i < kRows; i += 2) f = max3_abs(f, __uint_as_float(w[i][e]), __uint_as_float(w[i + 1][e]));
-        uint32_t m = __float_as_uint(f);
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-        if (lane < 16) wmax[warp][8 * c + e] = m;
+      for (int i = 0; i < kRows; ++i) {
+        const float scale = q8_scale(__shfl_sync(0xFFFFFFFFu, xs, (lane & 16) + i));
+        const uint32_t lo = w[i][0], hi = w[i][1];
+        float v[8];
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          q8_unpack2((p < 2 ? lo : hi) >> (16 * (p & 1)), a.x_e5m2 != 0, v[2 * p], v[2 * p + 1]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[i][e] = __float_as_uint(v[e] * scale);
       }
     }
-    __syncthreads();
-    if (threadIdx.x < kQ8Group) {
+    // elements 2p and 2p + 1 of row i
+    auto pair = [&](int i, int p) -> f2_t {
+      if constexpr (S == Src::kBf16)
+        return bf2_to_f2(w[i][p]);
+      else
+        return f2(__uint_as_float(w[i][2 * p]), __uint_as_float(w[i][2 * p + 1]));
+    };
+    // bit pattern of the largest magnitude of row i
+    auto row_max = [&](int i) -> uint32_t {
+      if constexpr (S == Src::kBf16) {
+        uint32_t m = __vmaxu2(__vmaxu2(w[i][0] & 0x7FFF7FFFu, w[i][1] & 0x7FFF7FFFu),
+                              __vmaxu2(w[i][2] & 0x7FFF7FFFu, w[i][3] & 0x7FFF7FFFu));
+        return max(m & 0xFFFF0000u, m << 16);
+      } else {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) m = max3_abs(m, __uint_as_float(w[i][e]), __uint_as_float(w[i][e + 1]));
+        return __float_as_uint(m);
+      }
+    };
+
+    uint32_t bsb = 0;
+    if constexpr (BLOCK) {
       uint32_t m = 0;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) m = max(m, wmax[k][threadIdx.x]);
-      const uint32_t sb = q8_scale_byte<E5M2>(m);
-      cinv[threadIdx.x] = q8_inv_scale(sb);
-      const int64_t col = tk * kQ8Group + threadIdx.x;
-      if (col < a.K) a.qt_scale[col * a.ldqt_scale + tm] = (uint8_t)sb;
+      for (int i = 0; i < kRows; ++i) m = max(m, row_max(i));
+      m = lanes_max<32>(m);
+      if (lane == 0) wmax[warp][0] = m;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) m = max(m, wmax[k][0]);
+      bsb = q8_scale_byte<E5M2>(m);
+      if (threadIdx.x == 0) {
+        if (a.q) a.q_scale[tm * a.ldq_scale + tk] = (uint8_t)bsb;
+        if (a.qt) a.qt_scale[tk * a.ldqt_scale + tm] = (uint8_t)bsb;
+      }
+    }
+    if (a.q) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        uint32_t sb = bsb;
+        if constexpr (!BLOCK) {
+          sb = q8_scale_byte<E5M2>(lanes_max<16>(row_max(i)));
+          if (c == 0 && row0 + i < a.M) a.q_scale[(row0 + i) * a.ldq_scale + tk] = (uint8_t)sb;
+        }
+        if (row0 + i >= a.M) continue;
+        const float inv = q8_inv_scale(sb);
+        const f2_t inv2 = f2(inv, inv);
+        float e[8];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) f2_split(f2_mul(pair(i, p), inv2), e[2 * p], e[2 * p + 1]);
+        store8(a.q + (row0 + i) * a.ldq + col0,
+               make_uint2(q8_pack4<E5M2>(e[0], e[1], e[2], e[3]), q8_pack4<E5M2>(e[4], e[5], e[6], e[7])), a.K - col0);
+      }
+    }
+    if (!a.qt) continue;
+
+    if constexpr (!BLOCK) {
+      // column maxima: this thread's rows, the warp's other row group, the warps
+      if constexpr (S == Src::kBf16) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          uint32_t m = w[0][p] & 0x7FFF7FFFu;
+#pragma unroll
+          for (int i = 1; i < kRows; ++i) m = __vmaxu2(m, w[i][p] & 0x7FFF7FFFu);
+          m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+          if (lane < 16) {
+            wmax[warp][8 * c + 2 * p] = m << 16;
+            wmax[warp][8 * c + 2 * p + 1] = m & 0xFFFF0000u;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float f = 0.f;
+#pragma unroll
+          for (int i = 0; i < kRows; i += 2) f = max3_abs(f, __uint_as_float(w[i][e]), __uint_as_float(w[i + 1][e]));
+          uint32_t m = __float_as_uint(f);
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+          if (lane < 16) wmax[warp][8 * c + e] = m;
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x < kQ8Group) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) m = max(m, wmax[k][threadIdx.x]);
+        const uint32_t sb = q8_scale_byte<E5M2>(m);
+        cinv[threadIdx.x] = q8_inv_scale(sb);
+        const int64_t col = tk * kQ8Group + threadIdx.x;
+        if (col < a.K) a.qt_scale[col * a.ldqt_scale + tm] = (uint8_t)sb;
+      }
+      __syncthreads();
+    }
+    const float binv = q8_inv_scale(bsb);
+    uint32_t* words = reinterpret_cast<uint32_t*>(tile);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float2 ci = BLOCK ? make_float2(binv, binv) : *reinterpret_cast<const float2*>(&cinv[8 * c + 2 * p]);
+      const f2_t inv2 = f2(ci.x, ci.y);
+      float lo[kRows], hi[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) f2_split(f2_mul(pair(i, p), inv2), lo[i], hi[i]);
+      // 8-byte word r of column k (rows 8r..) at slot r ^ (k / 8)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float* f = h ? hi : lo;
+        const int k = 8 * c + 2 * p + h;
+        if constexpr (kRows == 8)
+          tile[k * 16 + (g ^ c)] = make_uint2(q8_pack4<E5M2>(f[0], f[1], f[2], f[3]), q8_pack4<E5M2>(f[4], f[5], f[6], f[7]));
+        else
+          words[(k * 16 + ((g >> 1) ^ c)) * 2 + (g & 1)] = q8_pack4<E5M2>(f[0], f[1], f[2], f[3]);
+      }
     }
     __syncthreads();
-  }
-  const float binv = q8_inv_scale(bsb);
-  uint32_t* words = reinterpret_cast<uint32_t*>(tile);
+    // 16 bytes a lane: words 2j and 2j + 1 of column k, swapped where k / 8 is odd
+    const int j = threadIdx.x & 7;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const float2 ci = BLOCK ? make_float2(binv, binv) : *reinterpret_cast<const float2*>(&cinv[8 * c + 2 * p]);
-    const f2_t inv2 = f2(ci.x, ci.y);
-    float lo[kRows], hi[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) f2_split(f2_mul(pair(i, p), inv2), lo[i], hi[i]);
-    // 8-byte word r of column k (rows 8r..) at slot r ^ (k / 8)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float* f = h ? hi : lo;
-      const int k = 8 * c + 2 * p + h;
-      if constexpr (kRows == 8)
-        tile[k * 16 + (g ^ c)] = make_uint2(q8_pack4<E5M2>(f[0], f[1], f[2], f[3]), q8_pack4<E5M2>(f[4], f[5], f[6], f[7]));
-      else
-        words[(k * 16 + ((g >> 1) ^ c)) * 2 + (g & 1)] = q8_pack4<E5M2>(f[0], f[1], f[2], f[3]);
+    for (int k = threadIdx.x >> 3; k < kQ8Group; k += kThreads / 8) {
+      const int64_t col = tk * kQ8Group + k, row = tm * kQ8Group + 16 * j;
+      const int kc = k >> 3;
+      uint4 u = reinterpret_cast<const uint4*>(tile)[k * 8 + (j ^ (kc >> 1))];
+      if (kc & 1) u = make_uint4(u.z, u.w, u.x, u.y);
+      if (col < a.K && row < a.M) store16(a.qt + col * a.ldqt + row, u, a.M - row);
     }
-  }
-  __syncthreads();
-  // 16 bytes a lane: words 2j and 2j + 1 of column k, swapped where k / 8 is odd
-  const int j = threadIdx.x & 7;
-#pragma unroll
-  for (int k = threadIdx.x >> 3; k < kQ8Group; k += kThreads / 8) {
-    const int64_t col = tk * kQ8Group + k, row = tm * kQ8Group + 16 * j;
-    const int kc = k >> 3;
-    uint4 u = reinterpret_cast<const uint4*>(tile)[k * 8 + (j ^ (kc >> 1))];
-    if (kc & 1) u = make_uint4(u.z, u.w, u.x, u.y);
-    if (col < a.K && row < a.M) store16(a.qt + col * a.ldqt + row, u, a.M - row);
   }
 }
 
 template <Src S>
-cudaError_t launch_src(const QuantArgs& a, bool e5m2, bool block, unsigned grid, cudaStream_t st) {
-  void (*k)(const QuantArgs) =
+cudaError_t launch_src(const QuantArgs& a, bool e5m2, bool block, cudaStream_t st) {
+  void (*k)(const QuantArgs, const CUtensorMap) =
       e5m2 ? (block ? sp_quant_q8_kernel<S, true, true> : sp_quant_q8_kernel<S, true, false>)
            : (block ? sp_quant_q8_kernel<S, false, true> : sp_quant_q8_kernel<S, false, false>);
-  return pdl_launch(k, dim3(grid), dim3(Shape<S>::kThreads), 0, st, a);
+  CUtensorMap map = {};
+  int64_t grid = a.tiles;
+  size_t smem = 0;
+  if (S == Src::kQ8) {
+    cudaError_t e = byte_map(a.x, a.M, a.K, a.ldx, kQ8Group, false, &map);
+    int dev = 0, sms = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    smem = 128 + kRing * kTileBytes;  // 128: the alignment of the copies' targets
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (grid > 2 * sms) grid = 2 * sms;
+  }
+  return pdl_launch(k, dim3((unsigned)grid), dim3(Shape<S>::kThreads), smem, st, a, map);
 }
 
 }  // namespace
 
 cudaError_t launch_quant_q8(const QuantArgs& a, int x_dtype, bool e5m2, bool block, cudaStream_t st) {
-  const unsigned grid = (unsigned)((a.M + kQ8Group - 1) / kQ8Group * a.ktiles);
   switch (x_dtype) {
-    case SP_ELEM_F32: return launch_src<Src::kF32>(a, e5m2, block, grid, st);
-    case SP_ELEM_BF16: return launch_src<Src::kBf16>(a, e5m2, block, grid, st);
-    default: return launch_src<Src::kQ8>(a, e5m2, block, grid, st);
+    case SP_ELEM_F32: return launch_src<Src::kF32>(a, e5m2, block, st);
+    case SP_ELEM_BF16: return launch_src<Src::kBf16>(a, e5m2, block, st);
+    default: return launch_src<Src::kQ8>(a, e5m2, block, st);
   }
 }
 
