@@ -500,8 +500,8 @@ sp_status_t sp_quantize_q8(const sp_quantize_q8_desc_t* d, const void* x, const 
   a.q_scale = q_scale;
   a.qt = qt;
   a.qt_scale = qt_scale;
-  a.M = d->M;
-  a.K = d->K;
+  a.M = (int32_t)d->M;
+  a.K = (int32_t)d->K;
   a.ldx = d->ldx;
   a.ldq = d->ldq;
   a.ldqt = d->ldqt;
@@ -510,8 +510,7 @@ sp_status_t sp_quantize_q8(const sp_quantize_q8_desc_t* d, const void* x, const 
   a.ldqt_scale = d->ldqt_scale;
   a.ktiles = kg;
   a.tiles = mg * kg;
-  a.x_scale_rows = d->x_scale_rows;
-  a.x_e5m2 = d->x_dtype == SP_ELEM_E5M2;
+  a.x_scale_shift = d->x_scale_rows == kQ8Group ? 7 : 0;
   a.vec = aligned(x, 16) && d->ldx * xb % 16 == 0;
   if (inject_launch_failure()) return SP_ERR_CUDA;
   return from_cuda(launch_quant_q8(a, d->x_dtype, d->q_dtype == SP_ELEM_E5M2, d->block != 0,

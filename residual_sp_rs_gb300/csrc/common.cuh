@@ -497,13 +497,12 @@ struct QuantArgs {
   uint8_t* q_scale;
   uint8_t* qt;              // [K, M] or null
   uint8_t* qt_scale;
-  int64_t M, K;
+  int32_t M, K;
   int64_t ldx, ldq, ldqt;                      // elements between rows
   int64_t ldx_scale, ldq_scale, ldqt_scale;    // bytes between rows of scales
   int64_t ktiles;           // 128-column tiles
   int64_t tiles;            // 128 x 128 tiles
-  int32_t x_scale_rows;     // rows that share a scale of x: 1 or 128
-  int32_t x_e5m2;
+  int32_t x_scale_shift;    // 8-bit x: row r has its scales in row r >> this
   int32_t vec;              // x allows aligned vector loads
 };
 

@@ -34,7 +34,6 @@ enum class Src { kF32, kBf16, kQ8 };
 
 template <Src S>
 struct Shape {
-  static constexpr int kBytes = S == Src::kF32 ? 4 : 2;      // of an element (not asked for 8-bit input)
   static constexpr int kRows = S == Src::kBf16 ? 8 : 4;      // rows per thread
   static constexpr int kThreads = 16 * kQ8Group / kRows;
   static constexpr int kWords = S == Src::kBf16 ? 4 : 8;     // registers per row
@@ -49,11 +48,11 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 
 // Eight consecutive elements of a row from column `col` on, zero past K.
 template <Src S>
-__device__ __forceinline__ void load8(const QuantArgs& a, int64_t row, int64_t col, uint32_t (&w)[Shape<S>::kWords]) {
-  const char* p = static_cast<const char*>(a.x) + (row * a.ldx + col) * Shape<S>::kBytes;
-  if (a.vec && col + 8 <= a.K) {
+__device__ __forceinline__ void load8(const QuantArgs& a, int32_t row, int32_t col, uint32_t (&w)[Shape<S>::kWords]) {
+  const char* p = static_cast<const char*>(a.x) + ((int64_t)row * a.ldx + col) * (S == Src::kF32 ? 4 : 2);
+  if (a.vec && a.K - col >= 8) {
 #pragma unroll
-    for (int i = 0; i < Shape<S>::kBytes / 2; ++i) {
+    for (int i = 0; i < (S == Src::kF32 ? 4 : 2) / 2; ++i) {
       const uint4 u = ld_stream(p + 16 * i);
       w[4 * i] = u.x;
       w[4 * i + 1] = u.y;
@@ -66,7 +65,7 @@ __device__ __forceinline__ void load8(const QuantArgs& a, int64_t row, int64_t c
   for (int i = 0; i < Shape<S>::kWords; ++i) w[i] = 0u;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    if (col + e >= a.K) continue;
+    if (e >= a.K - col) continue;
     if constexpr (S == Src::kF32)
       w[e] = *(reinterpret_cast<const uint32_t*>(p) + e);
     else
@@ -75,7 +74,7 @@ __device__ __forceinline__ void load8(const QuantArgs& a, int64_t row, int64_t c
 }
 
 // Up to N (8 or 16) bytes to p, `n` of them inside the tensor.
-__device__ __forceinline__ void store8(uint8_t* p, uint2 w, int64_t n) {
+__device__ __forceinline__ void store8(uint8_t* p, uint2 w, int32_t n) {
   if (n >= 8) {
     *reinterpret_cast<uint2*>(p) = w;
     return;
@@ -84,7 +83,7 @@ __device__ __forceinline__ void store8(uint8_t* p, uint2 w, int64_t n) {
   for (int e = 0; e < 8; ++e)
     if (e < n) p[e] = (uint8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
 }
-__device__ __forceinline__ void store16(uint8_t* p, uint4 w, int64_t n) {
+__device__ __forceinline__ void store16(uint8_t* p, uint4 w, int32_t n) {
   if (n >= 16) {
     *reinterpret_cast<uint4*>(p) = w;
     return;
@@ -93,11 +92,12 @@ __device__ __forceinline__ void store16(uint8_t* p, uint4 w, int64_t n) {
   store8(p + 8, make_uint2(w.z, w.w), n - 8);
 }
 
-template <Src S, bool E5M2, bool BLOCK>
+template <Src S, bool E5M2, bool BLOCK, bool XE5M2>
 __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads) sp_quant_q8_kernel(const QuantArgs a, const __grid_constant__ CUtensorMap map) {
   constexpr int kRows = Shape<S>::kRows, kThreads = Shape<S>::kThreads, kWarps = kThreads / 32;
-  __shared__ uint32_t wmax[kWarps][kQ8Group];          // column maxima of each warp
-  __shared__ float cinv[kQ8Group];                     // 2^-s of each column
+  // column 8c + e: maxima of each warp at 17e + c, 2^-s at 2c + (e & 1) of pair e / 2
+  __shared__ uint32_t wmax[kWarps][8 * 17];
+  __shared__ float cinv[4][32];
   __shared__ __align__(16) uint2 tile[kQ8Group * 16];  // transposed bytes
 
   const int c = threadIdx.x & 15, g = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -116,26 +116,29 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
   grid_dep_launch_dependents();
 
   // 8-bit x: tile `t` to stage `s` of the ring
-  auto fetch = [&](int64_t t, int s) {
-    if (t >= a.tiles) return;
+  auto fetch = [&](uint32_t t, int s) {
+    if (t >= (uint32_t)a.tiles) return;
+    const uint32_t tm = t / (uint32_t)a.ktiles, tk = t - tm * (uint32_t)a.ktiles;
     mbar_arrive_expect_tx(&landed[s], kTileBytes);
-    tma_load_2d<1>(smem_addr(ring) + s * kTileBytes, &map, (int32_t)(t % a.ktiles * kQ8Group),
-                   (int32_t)(t / a.ktiles * kQ8Group), smem_addr(&landed[s]));
+    tma_load_2d<1>(smem_addr(ring) + s * kTileBytes, &map, (int32_t)(tk * kQ8Group), (int32_t)(tm * kQ8Group),
+                   smem_addr(&landed[s]));
   };
   if constexpr (S == Src::kQ8)
     if (threadIdx.x == 0)
-      for (int s = 0; s < kRing; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+      for (int s = 0; s < kRing; ++s) fetch(blockIdx.x + s * gridDim.x, s);
   int stage = 0;
   uint32_t phase = 0;
 
-  for (int64_t t = blockIdx.x; t < a.tiles; t += gridDim.x) {
-    const int64_t tm = t / a.ktiles, tk = t - tm * a.ktiles;
-    const int64_t row0 = tm * kQ8Group + kRows * g, col0 = tk * kQ8Group + 8 * c;
+  // tiles, rows and columns stay below 2^31; a.tiles + kRing * gridDim.x below 2^32
+  for (uint32_t t = blockIdx.x; t < (uint32_t)a.tiles; t += gridDim.x) {
+    const uint32_t tm = t / (uint32_t)a.ktiles, tk = t - tm * (uint32_t)a.ktiles;
+    const int32_t row0 = (int32_t)tm * kQ8Group + kRows * g, col0 = (int32_t)tk * kQ8Group + 8 * c;
+    const int32_t rows = a.M - row0;  // of this thread's inside the tensor (may be more, or negative)
     uint32_t w[kRows][Shape<S>::kWords] = {};
     uint32_t xs = 127u;  // 8-bit x: lane i of the 16 that share rows holds row i's scale byte
     if constexpr (S == Src::kQ8)
-      if (c < kRows && row0 + c < a.M)
-        xs = a.x_scale[(row0 + c) / a.x_scale_rows * a.ldx_scale + tk];
+      if (c < kRows && c < rows)
+        xs = a.x_scale[(int64_t)((row0 + c) >> a.x_scale_shift) * a.ldx_scale + tk];
     if constexpr (S == Src::kQ8) {
       const bool ok = mbar_wait(&landed[stage], phase, kWaitNs);
 #pragma unroll
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
         w[i][1] = ok ? u.y : 0x7F7F7F7Fu;
       }
       __syncthreads();  // the stage, and the last tile's words and maxima, have been read
-      if (threadIdx.x == 0) fetch(t + (int64_t)kRing * gridDim.x, stage);
+      if (threadIdx.x == 0) fetch(t + kRing * gridDim.x, stage);
       if (++stage == kRing) {
         stage = 0;
         phase ^= 1u;
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
     } else {
 #pragma unroll
       for (int i = 0; i < kRows; ++i)
-        if (row0 + i < a.M) load8<S>(a, row0 + i, col0, w[i]);
+        if (i < rows) load8<S>(a, row0 + i, col0, w[i]);
     }
     if constexpr (S == Src::kQ8) {
 #pragma unroll
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
         float v[8];
 #pragma unroll
         for (int p = 0; p < 4; ++p)
-          q8_unpack2((p < 2 ? lo : hi) >> (16 * (p & 1)), a.x_e5m2 != 0, v[2 * p], v[2 * p + 1]);
+          q8_unpack2((p < 2 ? lo : hi) >> (16 * (p & 1)), XE5M2, v[2 * p], v[2 * p + 1]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[i][e] = __float_as_uint(v[e] * scale);
       }
@@ -211,15 +214,15 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
         uint32_t sb = bsb;
         if constexpr (!BLOCK) {
           sb = q8_scale_byte<E5M2>(lanes_max<16>(row_max(i)));
-          if (c == 0 && row0 + i < a.M) a.q_scale[(row0 + i) * a.ldq_scale + tk] = (uint8_t)sb;
+          if (c == 0 && i < rows) a.q_scale[(int64_t)(row0 + i) * a.ldq_scale + tk] = (uint8_t)sb;
         }
-        if (row0 + i >= a.M) continue;
+        if (i >= rows) continue;
         const float inv = q8_inv_scale(sb);
         const f2_t inv2 = f2(inv, inv);
         float e[8];
 #pragma unroll
         for (int p = 0; p < 4; ++p) f2_split(f2_mul(pair(i, p), inv2), e[2 * p], e[2 * p + 1]);
-        store8(a.q + (row0 + i) * a.ldq + col0,
+        store8(a.q + (int64_t)(row0 + i) * a.ldq + col0,
                make_uint2(q8_pack4<E5M2>(e[0], e[1], e[2], e[3]), q8_pack4<E5M2>(e[4], e[5], e[6], e[7])), a.K - col0);
       }
     }
@@ -235,8 +238,8 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
           for (int i = 1; i < kRows; ++i) m = __vmaxu2(m, w[i][p] & 0x7FFF7FFFu);
           m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
           if (lane < 16) {
-            wmax[warp][8 * c + 2 * p] = m << 16;
-            wmax[warp][8 * c + 2 * p + 1] = m & 0xFFFF0000u;
+            wmax[warp][17 * (2 * p) + c] = m << 16;
+            wmax[warp][17 * (2 * p + 1) + c] = m & 0xFFFF0000u;
           }
         }
       } else {
@@ -247,18 +250,19 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
           for (int i = 0; i < kRows; i += 2) f = max3_abs(f, __uint_as_float(w[i][e]), __uint_as_float(w[i + 1][e]));
           uint32_t m = __float_as_uint(f);
           m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-          if (lane < 16) wmax[warp][8 * c + e] = m;
+          if (lane < 16) wmax[warp][17 * e + c] = m;
         }
       }
       __syncthreads();
       if (threadIdx.x < kQ8Group) {
+        const int e = threadIdx.x & 7, cc = threadIdx.x >> 3;
         uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) m = max(m, wmax[k][threadIdx.x]);
+        for (int k = 0; k < kWarps; ++k) m = max(m, wmax[k][17 * e + cc]);
         const uint32_t sb = q8_scale_byte<E5M2>(m);
-        cinv[threadIdx.x] = q8_inv_scale(sb);
-        const int64_t col = tk * kQ8Group + threadIdx.x;
-        if (col < a.K) a.qt_scale[col * a.ldqt_scale + tm] = (uint8_t)sb;
+        cinv[e >> 1][2 * cc + (e & 1)] = q8_inv_scale(sb);
+        const int32_t col = (int32_t)tk * kQ8Group + threadIdx.x;
+        if (col < a.K) a.qt_scale[(int64_t)col * a.ldqt_scale + tm] = (uint8_t)sb;
       }
       __syncthreads();
     }
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
     uint32_t* words = reinterpret_cast<uint32_t*>(tile);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const float2 ci = BLOCK ? make_float2(binv, binv) : *reinterpret_cast<const float2*>(&cinv[8 * c + 2 * p]);
+      const float2 ci = BLOCK ? make_float2(binv, binv) : *reinterpret_cast<const float2*>(&cinv[p][2 * c]);
       const f2_t inv2 = f2(ci.x, ci.y);
       float lo[kRows], hi[kRows];
 #pragma unroll
@@ -287,24 +291,24 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
     const int j = threadIdx.x & 7;
 #pragma unroll
     for (int k = threadIdx.x >> 3; k < kQ8Group; k += kThreads / 8) {
-      const int64_t col = tk * kQ8Group + k, row = tm * kQ8Group + 16 * j;
+      const int32_t col = (int32_t)tk * kQ8Group + k, row = (int32_t)tm * kQ8Group + 16 * j;
       const int kc = k >> 3;
       uint4 u = reinterpret_cast<const uint4*>(tile)[k * 8 + (j ^ (kc >> 1))];
       if (kc & 1) u = make_uint4(u.z, u.w, u.x, u.y);
-      if (col < a.K && row < a.M) store16(a.qt + col * a.ldqt + row, u, a.M - row);
+      if (col < a.K && row < a.M) store16(a.qt + (int64_t)col * a.ldqt + row, u, a.M - row);
     }
   }
 }
 
-template <Src S>
+template <Src S, bool XE5M2 = false>
 cudaError_t launch_src(const QuantArgs& a, bool e5m2, bool block, cudaStream_t st) {
   void (*k)(const QuantArgs, const CUtensorMap) =
-      e5m2 ? (block ? sp_quant_q8_kernel<S, true, true> : sp_quant_q8_kernel<S, true, false>)
-           : (block ? sp_quant_q8_kernel<S, false, true> : sp_quant_q8_kernel<S, false, false>);
+      e5m2 ? (block ? sp_quant_q8_kernel<S, true, true, XE5M2> : sp_quant_q8_kernel<S, true, false, XE5M2>)
+           : (block ? sp_quant_q8_kernel<S, false, true, XE5M2> : sp_quant_q8_kernel<S, false, false, XE5M2>);
   CUtensorMap map = {};
   int64_t grid = a.tiles;
   size_t smem = 0;
-  if (S == Src::kQ8) {
+  if constexpr (S == Src::kQ8) {
     cudaError_t e = byte_map(a.x, a.M, a.K, a.ldx, kQ8Group, false, &map);
     int dev = 0, sms = 0;
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
@@ -323,6 +327,7 @@ cudaError_t launch_quant_q8(const QuantArgs& a, int x_dtype, bool e5m2, bool blo
   switch (x_dtype) {
     case SP_ELEM_F32: return launch_src<Src::kF32>(a, e5m2, block, st);
     case SP_ELEM_BF16: return launch_src<Src::kBf16>(a, e5m2, block, st);
+    case SP_ELEM_E5M2: return launch_src<Src::kQ8, true>(a, e5m2, block, st);
     default: return launch_src<Src::kQ8>(a, e5m2, block, st);
   }
 }
