@@ -394,14 +394,14 @@ def _on(device, stream):
     return _on_stream(device, stream)
 
 
-def _same_device(first, *others):
-    """The index of the CUDA device that every tensor is on."""
-    dev = first.get_device()
+def _same_device(*tensors):
+    """The index of the CUDA device that every tensor (or None) is on."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}: all must be on one device")
     if dev < 0:
         raise ValueError("libspfuse takes CUDA tensors")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on {first.device} and {t.device}: all must be on one device")
     return dev
 
 
@@ -413,18 +413,24 @@ def _q8_operand(name, t, scale):
     """(address, row stride, scales' address, their row stride, rows per scale) of an 8-bit tensor."""
     if t.dtype not in _Q8_CODE:
         raise ValueError(f"{name}: float8_e4m3fn or float8_e5m2 expected, got {t.dtype}")
-    if scale is None or scale.dtype not in _SCALE_DTYPES or len(scale.shape) != 2 or len(t.shape) != 2:
+    if scale is None or scale.dtype not in _SCALE_DTYPES:
+        raise ValueError(f"{name}: a matrix of scale bytes expected")
+    shape, sshape = t.shape, scale.shape
+    if len(shape) != 2 or len(sshape) != 2:
         raise ValueError(f"{name}: a matrix and its matrix of scale bytes expected")
-    (rows, cols), (srows, groups) = t.shape, scale.shape
+    rows, cols = shape
+    srows, groups = sshape
     if groups != (cols + 127) // 128 or (srows != rows and srows != (rows + 127) // 128):
-        raise ValueError(f"{name}: values {tuple(t.shape)} do not go with scales {tuple(scale.shape)}")
-    p, ld = _rows2d(t)
-    s, lds = _rows2d(scale)
+        raise ValueError(f"{name}: values {tuple(shape)} do not go with scales {tuple(sshape)}")
+    ld, step = t.stride()
+    lds, sstep = scale.stride()
+    if (step != 1 and cols > 1) or (sstep != 1 and groups > 1):
+        raise ValueError(f"{name}: libspfuse takes matrices with dense rows")
     if rows <= 1 or groups == 0:  # the stride is not used, and a view may carry any
-        ld, lds = _ld16(ld), _ld16(lds)
+        ld, lds = _ld16(cols), _ld16(groups)
     elif srows == 1:
-        lds = _ld16(lds)
-    return p, ld, s, lds, 1 if srows == rows else Q8_GROUP
+        lds = _ld16(groups)
+    return t.data_ptr(), ld, scale.data_ptr(), lds, 1 if srows == rows else Q8_GROUP
 
 
 def forward_q8(desc: SpRsDesc, partials, residual, gamma, beta=None, stream=None, store_mask: bool = True) -> dict:
