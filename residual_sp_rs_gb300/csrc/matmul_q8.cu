@@ -125,14 +125,17 @@ __device__ __forceinline__ void store_piece(const MatmulArgs& a, const unsigned 
       *p = o;
     }
   } else {
-    for (int r = 0; r < rows; ++r)
-      for (int j = lane; j < ny; j += 32) {
+    for (int j = lane; j < ny; j += 32) {
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r) {
+        if (r >= rows) continue;
         T o = *reinterpret_cast<const T*>(buf + r * 128 + (((j / kPer) ^ (r & 7)) << 4) + sizeof(T) * (j % kPer));
         T* p = c + r * a.ldc + j;
         if constexpr (sizeof(T) == 4)
           if (a.accumulate) o += *p;
         *p = o;
       }
+    }
   }
 }
 
@@ -518,19 +521,25 @@ int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 //   x BN x 128), its loads (56 bytes a clock from L2 to an SM: 128 x 256 tiles
 //   0.46, pairs 0.35, 128 x 128 tiles 0.28 us a block) and the issue of its
 //   instructions (0.22 us whatever BN is);
-//   starting and ending a kernel 2.6 us, the last tile's epilogue 19 clocks a
-//   column (90 with the operands swapped, whose stores are narrow), a pair's
-//   cluster barriers and the turns of its tiles more than a single CTA's
-//   (4096 x 1536 x 768 in 192 columns: 9.4 us single, 11.4 us paired; 16384 x
-//   4096 x 8192 in 256 columns: 333 and 291 us);
+//   an epilogue takes 0.8 us per 128 columns of bf16, 0.45 us per 64 of fp32, a
+//   sixth more where the tile cuts a piece of a row, five times that where C's
+//   rows are not aligned (2305 x 4999 x 129 in 128 columns: 23 us), and 90
+//   clocks a column with the operands swapped, whose stores are narrow; it runs
+//   under the next tile's products;
+//   starting and ending a kernel costs 2.6 us, a pair's cluster barriers and the
+//   turns of its tiles more than a single CTA's (4096 x 1536 x 768 in 192
+//   columns: 9.4 us single, 11.4 us paired; 16384 x 4096 x 8192 in 256 columns:
+//   333 and 291 us);
 //   nothing is faster than its bytes from memory.
 Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
-  constexpr double kLoadRate = 56.0, kIssue = 430.0, kStart = 5200.0, kColumn = 19.0, kSwapColumn = 90.0, kJoin = 1500.0;
-  constexpr double kPair = 2000.0, kPairTurn = 2500.0, kMemoryRate = 3300.0;
+  constexpr double kLoadRate = 56.0, kIssue = 430.0, kStart = 5200.0, kSwapColumn = 90.0, kJoin = 1500.0, kMemoryRate = 3300.0;
+  constexpr double kRoundF32 = 900.0, kRoundBf16 = 1600.0, kScalar = 5.0, kRagged = 1.15;
+  constexpr double kPair = 2000.0, kPairTurn = 2500.0, kTurn = 800.0, kSwapTurn = 5000.0;
   Choice ch = {1, false};
   double least = 1e300;
   const double memory = ((double)(a.M + a.N) * a.K + (double)a.M * a.N * (a.c_f32 ? 4 : 2)) / kMemoryRate;
   const int64_t nkb = ceil_div(a.K, 128);
+  const int piece = a.c_f32 ? 32 : 64;  // columns of C in a 128-byte piece of a row
   for (int mode = 0; mode < 3; ++mode) {  // one CTA, a pair of CTAs, one CTA with the operands swapped
     const int cg = mode == 1 ? 2 : 1;
     const bool swap = mode == 2;
@@ -547,9 +556,12 @@ Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
         const int64_t ctas = xt * yt * ks * cg;
         const int64_t turns = ceil_div(ctas, per_sm * sms / cg * cg);
         const double load = (kXRows + BN / cg) * 128 / kLoadRate * (ctas > sms ? per_sm : 1);
-        const double path = (double)turns * (ceil_div(nkb, ks) * fmax(fmax(2.0 * BN, load), kIssue) + (cg == 2 ? kPairTurn : 0.0));
-        const double t = kStart + fmax(path, memory) + 0.1 * path + (swap ? kSwapColumn : kColumn) * BN +
-                         (cg == 2 ? kPair : 0.0) + (ks > 1 ? kJoin : 0.0);
+        const int64_t rounds = ceil_div(ceil_div(BN, piece), 2);  // pieces of a row that each epilogue warp takes
+        const double epilogue = swap ? kSwapColumn * BN : rounds * (a.c_f32 ? kRoundF32 : kRoundBf16) *
+                                                              (a.c_vec ? 1.0 : kScalar) * (BN % piece ? kRagged : 1.0);
+        const double main = ceil_div(nkb, ks) * fmax(fmax(2.0 * BN, load), kIssue);
+        const double path = turns * fmax(main, epilogue) + (cg == 2 ? turns * kPairTurn : swap ? (turns - 1) * kSwapTurn : turns * kTurn);
+        const double t = kStart + fmax(path, memory) + 0.1 * path + epilogue + (cg == 2 ? kPair : 0.0) + (ks > 1 ? kJoin : 0.0);
         if (t < least) {
           least = t;
           ch = {cg, swap};

@@ -26,6 +26,8 @@ communication around the fused kernels; all arithmetic stays in libspfuse:
   d_sum all-gathered (``post_chunk_gather``) while the next chunk computes
   (``sp_rs_dropout_residual_norm_bwd_rows``, dgamma/dbeta accumulated over
   the chunks in order).
+* ``gather_q8``: the all-gather of the norm's output in 8 bits with its scales
+  (``ops.forward_q8``), in front of an 8-bit column-parallel product.
 * ``allreduce_norm_grads``: dgamma/dbeta are per-shard partial sums; the
   replicated norm weights need their sum over ranks (MiniMind-tron ch.3,
   §3.4.2.1).
@@ -176,6 +178,28 @@ def forward_pipelined(desc, partial: torch.Tensor, residual, gamma, beta, h_out,
                                                  residual, gamma, beta, h_out, y_out, mask_out, rstd_out,
                                                  mean_out)
     return recv
+
+
+def gather_q8(q: torch.Tensor, scale: torch.Tensor, group=None):
+    """The all-gather in front of a column-parallel product, in 8 bits: half
+    the bytes of a 16-bit norm output.  q [R, H] and scale [R, ceil(H/128)]:
+    this rank's shard as ``ops.forward_q8`` returns it.  Returns (q, scale) of
+    all T*R rows, in rank order, with the row strides that ``ops.matmul_q8``
+    takes.  A row's scales are its own, so any R will do."""
+    T = dist.get_world_size(group)
+    out = []
+    for t in (q, scale):
+        R, C = t.shape
+        ld = ops._ld16(C)
+        if t.is_contiguous() and ld == C:
+            rows = t.view(torch.uint8)
+        else:  # whole 16-byte rows travel
+            rows = torch.zeros((R, ld), dtype=torch.uint8, device=t.device)
+            rows[:, :C] = t.view(torch.uint8)
+        full = torch.empty((T * R, ld), dtype=torch.uint8, device=t.device)
+        dist.all_gather_into_tensor(full, rows, group=group)
+        out.append(full[:, :C].view(t.dtype))
+    return out[0], out[1]
 
 
 def post_chunk_gather(d_sum: torch.Tensor, grad: torch.Tensor, R: int, b: int, e: int, group=None):

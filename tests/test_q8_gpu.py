@@ -245,9 +245,9 @@ def test_matmul_exact_sums(M, N, K, af, bf, ablock, bblock):
 
 
 @pytest.mark.parametrize("M,N,K", [(1300, 2600, 200), (4000, 1500, 256), (2305, 4999, 129), (4096, 4104, 384),
-                                   (9000, 520, 1100)])
+                                   (9000, 520, 1100), (2304, 4096, 4200), (2300, 4099, 4200), (1000, 4100, 4200)])
 def test_matmul_exact_sums_many_tiles(M, N, K):
-    """Several tiles per CTA or CTA pair, ragged on every side."""
+    """Several tiles per CTA or (the longer K) CTA pair, ragged on every side."""
     g = gen(M + N)
     a, sa, av = exact8(g, M, K, "e4m3", False)
     b, sb, bv = exact8(g, N, K, "e4m3", True)
@@ -545,3 +545,45 @@ def test_status_word_stays_clear():
     b, sb, bv = exact8(g, 100, 500, "e4m3", False)
     assert same(ops.matmul_q8(a, sa, b, sb, out_dtype=F32, status=word), av @ bv.t())
     assert int(word) == 0
+
+
+# ---- bounded waits --------------------------------------------------------------------------------
+
+TIMEOUT_SHAPES = [(1300, 2600, 200), (1000, 4100, 4200), (9, 1000, 4096)]   # single CTAs, pairs, K split in a cluster
+
+
+def _timeout_child(path):
+    out = []
+    for M, N, K in TIMEOUT_SHAPES:
+        g = gen(M)
+        a, sa, _ = exact8(g, M, K, "e4m3", False)
+        b, sb, _ = exact8(g, N, K, "e4m3", True)
+        word = torch.zeros(1, dtype=torch.int32, device=DEV)
+        c = ops.matmul_q8(a, sa, b, sb, out_dtype=F32, status=word)
+        torch.cuda.synchronize()
+        out.append((c.cpu(), int(word)))
+    torch.save(out, path)
+
+
+def test_timed_out_wait_marks_its_tiles_and_sets_the_status_word(tmp_path):
+    """The library's test hooks shorten the waits to 2 ms and make CTA 0 skip one stage, so that the waits on it run
+    out: the kernel returns, that CTA's tiles are NaN, all others are right, and the status word says so."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    path = str(tmp_path / "child.pt")
+    env = dict(os.environ, SPFUSE_TEST_WAIT_NS="2000000", SPFUSE_TEST_DROP_STAGE="1")
+    code = f"import sys; sys.path.insert(0, {root!r}); from tests.test_q8_gpu import _timeout_child; _timeout_child({path!r})"
+    r = subprocess.run([sys.executable, "-c", code], env=env, cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    for (M, N, K), (c, word) in zip(TIMEOUT_SHAPES, torch.load(path)):
+        g = gen(M)
+        a, sa, av = exact8(g, M, K, "e4m3", False)
+        b, sb, bv = exact8(g, N, K, "e4m3", True)
+        want = (av.to(DEV) @ bv.to(DEV).t()).float().cpu()
+        bad = c.isnan()
+        assert word == 0x4 and bool(bad.any()) and not bool(bad.all())
+        assert torch.equal(c[~bad], want[~bad])
+        word = torch.zeros(1, dtype=torch.int32, device=DEV)   # and without the hooks
+        assert torch.equal(ops.matmul_q8(a, sa, b, sb, out_dtype=F32, status=word).cpu(), want) and int(word) == 0

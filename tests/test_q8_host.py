@@ -174,3 +174,38 @@ def test_q8_empty_strides(spf):
     for cols in (0, 1, 15, 16, 17, 128):
         t = spf.q8_empty(3, cols, "cpu")
         assert t.shape == (3, cols) and t.stride(0) % 16 == 0 and t.stride(0) >= cols
+
+
+# ---- the gather across ranks -----------------------------------------------------------
+
+def _gather_rank(rank, world, port, out, R, H):
+    import torch.distributed as dist
+    sys.path.insert(0, ROOT)
+    os.environ.update(MASTER_ADDR="127.0.0.1", MASTER_PORT=str(port))
+    dist.init_process_group("gloo", rank=rank, world_size=world)
+    from residual_sp_rs_gb300 import ops, sp_exchange as ex
+    g = torch.Generator().manual_seed(rank)
+    q = ops.q8_empty(R, H, "cpu")
+    s = ops.q8_empty(R, -(-H // 128), "cpu")
+    q.copy_(torch.randint(0, 256, (R, H), generator=g))
+    s.copy_(torch.randint(0, 256, s.shape, generator=g))
+    fq, fs = ex.gather_q8(q.view(torch.float8_e4m3fn), s)
+    assert fq.dtype == torch.float8_e4m3fn and fq.stride(0) % 16 == 0 and fs.stride(0) % 16 == 0
+    torch.save((q, s, fq.view(torch.uint8).clone(), fs.clone()), f"{out}.{rank}")
+    dist.barrier()
+    dist.destroy_process_group()
+
+
+@pytest.mark.parametrize("world,R,H", [(2, 3, 256), (2, 5, 264), (4, 1, 2048)])
+def test_gather_q8_on_gloo_ranks(tmp_path, world, R, H):
+    import socket
+
+    import torch.multiprocessing as mp
+    with socket.socket() as sock:
+        sock.bind(("127.0.0.1", 0))
+        port = sock.getsockname()[1]
+    out = str(tmp_path / "g")
+    mp.start_processes(_gather_rank, args=(world, port, out, R, H), nprocs=world, start_method="spawn")
+    parts = [torch.load(f"{out}.{r}") for r in range(world)]
+    for _, _, fq, fs in parts:
+        assert torch.equal(fq, torch.cat([p[0] for p in parts])) and torch.equal(fs, torch.cat([p[1] for p in parts]))
