@@ -60,6 +60,7 @@ struct MatmulPlan {
   int32_t nkb;           // 128-value blocks of K
   uint32_t tmem_cols;    // power of two
   uint32_t acc1;         // column of the second accumulator
+  int32_t overlap;       // the accumulators share columns
   uint32_t sf_col;       // first column of the scales
   uint32_t smem;
 };
@@ -67,7 +68,7 @@ struct MatmulPlan {
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t sf_full[kScaleSlots], sf_empty[kScaleSlots];
-  uint64_t acc_full, acc_free, drain;
+  uint64_t acc_full[2], acc_free[2], drain;  // of each accumulator
   uint32_t tmem;
 };
 
@@ -176,8 +177,10 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
       mbar_init(&sh.sf_full[s], 2 * CG);
       mbar_init(&sh.sf_empty[s], 1);
     }
-    mbar_init(&sh.acc_full, 1);
-    mbar_init(&sh.acc_free, epilogue_warps(SWAP) * CG);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.acc_full[i], 1);
+      mbar_init(&sh.acc_free[i], epilogue_warps(SWAP) * CG);
+    }
     mbar_init(&sh.drain, 1);
     fence_mbar_init();
   }
@@ -249,9 +252,11 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
       bool ok = true;
       for (int64_t t = first; t < tiles && ok; t += step, ++n) {
         const uint32_t d = tmem + (n & 1u ? p.acc1 : 0u);
-        // the accumulators may overlap in the columns that the epilogue of
-        // the tile before reads first; it has finished the tile before that
-        if (n > 0 && !(ok = wait(&sh.acc_free, (n - 1) & 1u))) break;
+        // The accumulators of a wide tile overlap in the columns that the
+        // epilogue of the tile before reads first; else this one is free once
+        // the tile before that has been read.
+        const uint32_t back = p.overlap ? 1u : 2u;
+        if (n >= back && !(ok = wait(&sh.acc_free[(n - back) & 1u], ((n - back) >> 1) & 1u))) break;
         bool landed = false;  // this stage's data, tested for while the products before it were issued
         for (int kb = kb0; kb < kb1; ++kb) {
           if (kb == kb0 || (kb & 3) == 0) {
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
           if (left > 96) umma_mxf8<CG>(d, dx + 6, dy + 6, id, sfx, sfy, 1u, one);
           umma_commit<CG>(done, one);
         }
-        if (ok) umma_commit<CG>(&sh.acc_full, one);
+        if (ok) umma_commit<CG>(&sh.acc_full[n & 1u], one);
       }
       if (!ok && lane == 0) report_status(a.status, kStatusMatmulWaitTimeout);
       umma_commit<CG>(&sh.drain, one);
@@ -351,16 +356,16 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
     // ---- epilogue -----------------------------------------------------------------
     const int w4 = warp & 3, half = (warp - 4) >> 2, halves = epilogue_warps(SWAP) / 4;
     unsigned char* stage_c = dsm + (uint32_t)p.stages * stage_bytes + kScaleSlots * sf_bytes + (warp - 4) * kStoreBytes;
-    // this warp has read its first columns of the tile (and every one of the
-    // tile before)
-    auto free_acc = [&]() {
+    // this warp has read the columns of tile n that the next products wait for.
+    // (Once per tile, after the tile is complete: no warp can be a phase ahead.)
+    auto free_acc = [&](uint32_t n) {
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (CG == 2)
-          mbar_arrive_cluster(map_cta(smem_addr(&sh.acc_free), 0));
+          mbar_arrive_cluster(map_cta(smem_addr(&sh.acc_free[n & 1u]), 0));
         else
-          mbar_arrive(&sh.acc_free);
+          mbar_arrive(&sh.acc_free[n & 1u]);
       }
     };
     uint32_t n = 0;
@@ -370,17 +375,21 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
       tile_at(p, t, tx, ty);
       const int64_t x = (tx * CG + (CG == 2 ? rank : 0)) * kXRows + 32 * w4 + lane, y0 = ty * p.BN;
       const uint32_t acc = tmem + (n & 1u ? p.acc1 : 0u) + ((uint32_t)(32 * w4) << 16);
-      if (kb0 < kb1 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&sh.acc_full, n & 1u, limit));
+      if (kb0 < kb1 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&sh.acc_full[n & 1u], (n >> 1) & 1u, limit));
       if (!ok && lane == 0 && w4 == 0) report_status(a.status, kStatusMatmulWaitTimeout);
       tmem_fence_after();
       // columns a chunk: 128 bytes of a row of C, the columns that the
       // accumulators may share first
       const int width = SWAP || a.c_f32 ? 32 : 64, chunks = (p.BN + width - 1) / width;
-      if (half >= chunks) free_acc();  // nothing to read for this warp
+      // The overlap is in the first piece of the first half's warps; without
+      // one the whole tile has to be read.
+      if (half >= chunks || (p.overlap && half > 0)) free_acc(n);
       for (int c = half; c < chunks; c += halves) {
         const int col0 = width * (n & 1u ? c : chunks - 1 - c);
         if (!SWAP) __syncwarp();  // the staged piece before this one has been read
-        for (int col = col0; col < min(col0 + width, p.BN); col += 32) {
+        const int pieces = (min(width, p.BN - col0) + 31) / 32;
+        for (int k = 0; k < pieces; ++k) {
+          const int col = col0 + 32 * (n & 1u ? k : pieces - 1 - k);
           uint32_t v[32];
           if (kb0 < kb1 && ok) {
             if (p.BN - col >= 32) {
@@ -396,6 +405,7 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = ok ? 0u : 0x7FC00000u;
           }
+          if (p.overlap ? half == 0 && c == 0 && k == 0 : c + halves >= chunks && k == pieces - 1) free_acc(n);
           if constexpr (SWAP) {
             const int ny = (int)min((int64_t)min(32, p.BN - col), YR - (y0 + col));  // columns inside C
             if (p.ks > 1) {
@@ -423,7 +433,6 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
             }
           }
         }
-        if (c == half) free_acc();
         if constexpr (!SWAP) {
           __syncwarp();
           const int ny = (int)min((int64_t)min(width, p.BN - col0), YR - (y0 + col0));
@@ -580,7 +589,8 @@ Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
   p.tmem_cols = pow2_at_least((p.ks > 1 ? p.BN : 2 * p.BN) + sf_cols);
   if (p.tmem_cols > 512) p.tmem_cols = 512;
   p.sf_col = p.tmem_cols - sf_cols;
-  p.acc1 = p.sf_col - p.BN;  // overlaps the first accumulator by less than 32 columns
+  p.acc1 = p.sf_col - p.BN;
+  p.overlap = (int)p.acc1 < p.BN;  // BN 256: by 16 columns (or a split's one accumulator)
   const uint32_t stage = kXBytes + (uint32_t)(p.BN / ch.cg) * 128u;
   const uint32_t rest = 1024 + kScaleSlots * kScaleAtom * (1 + scale_atoms_y(p.BN)) + (ch.swap ? 0 : epilogue_warps(false) * kStoreBytes);
   // 2048: the kernel's static shared memory and the driver's, rounded up.  A short side
