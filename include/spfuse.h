@@ -259,7 +259,7 @@ sp_status_t sp_quantize_q8(const sp_quantize_q8_desc_t* desc, const void* x,
  * layer y = x W^T: y from x and W; dx from dy and W^T; dW from dy^T and x^T
  * (the transposed tensors as sp_quantize_q8 makes them). */
 typedef struct sp_matmul_q8_desc_t {
-  int64_t M, N, K;        /* each below 2^31 */
+  int64_t M, N, K;        /* each below 2^31, and C below 2^31 tiles of 128 x 16 */
   int64_t lda, ldb;       /* bytes between rows of A and of B */
   int64_t lda_scale;      /* bytes between rows of their scales */
   int64_t ldb_scale;

@@ -530,6 +530,8 @@ sp_status_t sp_matmul_q8(const sp_matmul_q8_desc_t* d, const uint8_t* a, const u
   if (!aligned(d->status, 4)) return SP_ERR_ALIGN;
   if (d->M < 0 || d->N < 0 || d->K < 0 || d->M >= kMaxQ8Dim || d->N >= kMaxQ8Dim || d->K >= kMaxQ8Dim)
     return SP_ERR_SHAPE;
+  if (q8_groups(d->M) * ((d->N + 15) / 16) >= kMaxQ8Dim || q8_groups(d->N) * ((d->M + 15) / 16) >= kMaxQ8Dim)
+    return SP_ERR_SHAPE;  // tiles of C
   const int64_t am = d->a_scale_rows == 1 ? d->M : q8_groups(d->M), bn = d->b_scale_rows == 1 ? d->N : q8_groups(d->N);
   if (!q8_strides_ok(d->M, d->K, d->lda, am, d->lda_scale) || !q8_strides_ok(d->N, d->K, d->ldb, bn, d->ldb_scale))
     return SP_ERR_SHAPE;

@@ -76,11 +76,12 @@ __host__ __device__ constexpr uint32_t scale_atoms_y(int BN) { return (uint32_t)
 
 // Tile t of the list: `width` tiles of X, along Y, then the next ones, so that
 // the tiles in flight share their operands in L2.
-__device__ __forceinline__ void tile_at(const MatmulPlan& p, int64_t t, int64_t& tx, int64_t& ty) {
-  const int64_t w = p.width, per = w * p.ytiles, g = t / per, in = t - g * per;
-  const int64_t width = min(w, (int64_t)p.xtiles - g * w);
-  tx = g * w + in % width;
-  ty = in / width;
+// (32-bit: the two 64-bit divisions took 0.7 us a tile of every role's time.)
+__device__ __forceinline__ void tile_at(const MatmulPlan& p, uint32_t t, int32_t& tx, int32_t& ty) {
+  const uint32_t per = (uint32_t)p.width * (uint32_t)p.ytiles, g = t / per, in = t - g * per;
+  const uint32_t width = min((uint32_t)p.width, (uint32_t)p.xtiles - g * (uint32_t)p.width), row = in / width;
+  tx = (int32_t)(g * (uint32_t)p.width + (in - row * width));
+  ty = (int32_t)row;
 }
 
 __device__ __forceinline__ void store_one(const MatmulArgs& a, int64_t o, float v) {
@@ -108,22 +109,26 @@ __device__ __forceinline__ void store_piece(const MatmulArgs& a, const unsigned 
   T* c = static_cast<T*>(a.c) + x * a.ldc + y;
   const int rows = (int)min((int64_t)32, XR - x);
   if (a.c_vec && ny % kPer == 0) {
-    const int q = lane & 7;
+    const int q = lane & 7, r0 = lane >> 3;
     if (q * kPer >= ny) return;
+    uint4 o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      o[i] = *reinterpret_cast<const uint4*>(buf + (4 * i + r0) * 128 + ((q ^ ((4 * i + r0) & 7)) << 4));
+    T* p = c + r0 * a.ldc + kPer * q;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      if (r >= rows) break;
-      uint4 o = *reinterpret_cast<const uint4*>(buf + r * 128 + ((q ^ (r & 7)) << 4));
-      uint4* p = reinterpret_cast<uint4*>(c + r * a.ldc + kPer * q);
-      if constexpr (sizeof(T) == 4) {
-        if (a.accumulate) {
-          const float4 b = *reinterpret_cast<const float4*>(p);
-          o = make_uint4(__float_as_uint(__uint_as_float(o.x) + b.x), __float_as_uint(__uint_as_float(o.y) + b.y),
-                         __float_as_uint(__uint_as_float(o.z) + b.z), __float_as_uint(__uint_as_float(o.w) + b.w));
+      if (4 * i + r0 < rows) {
+        if constexpr (sizeof(T) == 4) {
+          if (a.accumulate) {
+            const float4 b = *reinterpret_cast<const float4*>(p);
+            o[i] = make_uint4(__float_as_uint(__uint_as_float(o[i].x) + b.x), __float_as_uint(__uint_as_float(o[i].y) + b.y),
+                              __float_as_uint(__uint_as_float(o[i].z) + b.z), __float_as_uint(__uint_as_float(o[i].w) + b.w));
+          }
         }
+        *reinterpret_cast<uint4*>(p) = o[i];
       }
-      *p = o;
+      p += 4 * a.ldc;
     }
   } else {
     for (int j = lane; j < ny; j += 32) {
@@ -157,10 +162,9 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
 
   // X is the operand whose rows fill the tensor core's 128 lanes
   const int64_t XR = SWAP ? a.N : a.M, YR = SWAP ? a.M : a.N;
-  const int64_t xt_pairs = p.xtiles;  // tiles of CG * 128 rows
-  const int64_t tiles = xt_pairs * p.ytiles;
-  const int group = CG * p.ks;                          // CTAs per tile
-  const int64_t first = blockIdx.x / group, step = gridDim.x / group;
+  const uint32_t tiles = (uint32_t)p.xtiles * (uint32_t)p.ytiles;  // below 2^31
+  const uint32_t group = CG * p.ks;                                // CTAs per tile
+  const uint32_t first = blockIdx.x / group, step = gridDim.x / group;
   const int split = CG == 1 ? (int)rank : 0;
   const int kb0 = (int)((int64_t)p.nkb * split / p.ks), kb1 = (int)((int64_t)p.nkb * (split + 1) / p.ks);
 
@@ -202,11 +206,11 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
       int s = 0, issued = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int64_t t = first; t < tiles && ok; t += step) {
-        int64_t tx, ty;
+      for (uint32_t t = first; t < tiles && ok; t += step) {
+        int32_t tx, ty;
         tile_at(p, t, tx, ty);
-        const int32_t x0 = (int32_t)(tx * CG + (CG == 2 ? rank : 0)) * kXRows;
-        const int32_t y0 = (int32_t)(ty * p.BN) + (CG == 2 ? (int32_t)rank * (p.BN / 2) : 0);
+        const int32_t x0 = (tx * CG + (CG == 2 ? (int32_t)rank : 0)) * kXRows;
+        const int32_t y0 = ty * p.BN + (CG == 2 ? (int32_t)rank * (p.BN / 2) : 0);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&sh.empty[s], ph ^ 1u, limit)) {
             ok = false;
@@ -250,17 +254,19 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
       uint32_t ph = 0, qph = 0;
       uint32_t n = 0;  // tiles of this CTA so far
       bool ok = true;
-      for (int64_t t = first; t < tiles && ok; t += step, ++n) {
+      for (uint32_t t = first; t < tiles && ok; t += step, ++n) {
         const uint32_t d = tmem + (n & 1u ? p.acc1 : 0u);
         // The accumulators of a wide tile overlap in the columns that the
         // epilogue of the tile before reads first; else this one is free once
         // the tile before that has been read.
         const uint32_t back = p.overlap ? 1u : 2u;
         if (n >= back && !(ok = wait(&sh.acc_free[(n - back) & 1u], ((n - back) >> 1) & 1u))) break;
-        bool landed = false;  // this stage's data, tested for while the products before it were issued
+        // this stage's data and the next scales, tested for while the products
+        // before them were issued
+        bool landed = false, scales = false;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (kb == kb0 || (kb & 3) == 0) {
-            if (!(ok = wait(&sh.sf_full[q], qph))) break;
+            if (!__all_sync(0xFFFFFFFFu, scales) && !(ok = wait(&sh.sf_full[q], qph))) break;
             const uint32_t src = sf_base + (uint32_t)q * sf_bytes;
             tmem_cp_scales<CG>(sfx, desc_rows16(src), one);
             tmem_cp_scales<CG>(sfy, desc_rows16(src + kScaleAtom), one);
@@ -282,7 +288,8 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
             s = 0;
             ph ^= 1u;
           }
-          landed = mbar_test(&sh.full[s], ph);
+          landed = mbar_test<false>(&sh.full[s], ph);
+          if ((kb & 3) == 3) scales = mbar_test<CG == 2>(&sh.sf_full[q], qph);
           // 32 bytes of K a step (2 in the descriptors' units), the last block only as far as K goes
           const uint32_t add = kb > kb0 ? 1u : 0u;
           const int64_t left = a.K - (int64_t)kb * 128;
@@ -309,10 +316,10 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
     int q = 0;
     uint32_t qph = 0;
     bool ok = true;
-    for (int64_t t = first; t < tiles && ok; t += step) {
-      int64_t tx, ty;
+    for (uint32_t t = first; t < tiles && ok; t += step) {
+      int32_t tx, ty;
       tile_at(p, t, tx, ty);
-      const int64_t x0 = (tx * CG + (CG == 2 ? rank : 0)) * kXRows, y0 = ty * p.BN;
+      const int64_t x0 = (int64_t)(tx * CG + (CG == 2 ? (int32_t)rank : 0)) * kXRows, y0 = (int64_t)ty * p.BN;
       uint4 w[6];  // the words of groups 4m .. 4m + 3 of rows tid, tid + 64, ... of X (128), then of Y
       for (int g = kb0 >> 2; g <= (kb1 - 1) >> 2 && kb0 < kb1; ++g) {
         if (g == kb0 >> 2 || (g & 3) == 0) {
@@ -370,10 +377,10 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
     };
     uint32_t n = 0;
     bool ok = true;
-    for (int64_t t = first; t < tiles; t += step, ++n) {
-      int64_t tx, ty;
+    for (uint32_t t = first; t < tiles; t += step, ++n) {
+      int32_t tx, ty;
       tile_at(p, t, tx, ty);
-      const int64_t x = (tx * CG + (CG == 2 ? rank : 0)) * kXRows + 32 * w4 + lane, y0 = ty * p.BN;
+      const int64_t x = (int64_t)(tx * CG + (CG == 2 ? (int32_t)rank : 0)) * kXRows + 32 * w4 + lane, y0 = (int64_t)ty * p.BN;
       const uint32_t acc = tmem + (n & 1u ? p.acc1 : 0u) + ((uint32_t)(32 * w4) << 16);
       if (kb0 < kb1 && ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&sh.acc_full[n & 1u], (n >> 1) & 1u, limit));
       if (!ok && lane == 0 && w4 == 0) report_status(a.status, kStatusMatmulWaitTimeout);
@@ -453,15 +460,15 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
   } else if (p.ks > 1) {
     cluster_sync();  // one tile per cluster: every CTA's part is in its shared memory
     if constexpr (SWAP) {
-      int64_t tx, ty;
+      int32_t tx, ty;
       tile_at(p, first, tx, ty);
       const int l = threadIdx.x & 127;
-      const int64_t x = tx * kXRows + l;
-      const int cols = (int)min((int64_t)p.BN, YR - ty * p.BN);
+      const int64_t x = (int64_t)tx * kXRows + l;
+      const int cols = (int)min((int64_t)p.BN, YR - (int64_t)ty * p.BN);
       for (int col = (int)rank + p.ks * (threadIdx.x >> 7); col < cols; col += threads(SWAP) / 128 * p.ks) {
         float sum = 0.f;
         for (int r = 0; r < p.ks; ++r) sum += ld_cluster_f32(map_cta(base + (uint32_t)(col * kXRows + l) * 4u, r));
-        if (x < XR) store_one(a, (ty * p.BN + col) * a.ldc + x, sum);
+        if (x < XR) store_one(a, ((int64_t)ty * p.BN + col) * a.ldc + x, sum);
       }
     }
     cluster_sync();  // nobody's shared memory goes before it is read
@@ -527,23 +534,22 @@ int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 // Tile shape and split of K: the least of an estimate of the time, in clocks,
 // whose constants are measured (back to back on one GB300 at about 2 GHz):
 //   a block of K costs a CTA the largest of its products (2 BN clocks for 128
-//   x BN x 128), its loads (56 bytes a clock from L2 to an SM: 128 x 256 tiles
-//   0.46, pairs 0.35, 128 x 128 tiles 0.28 us a block) and the issue of its
-//   instructions (0.22 us whatever BN is);
-//   an epilogue takes 0.8 us per 128 columns of bf16, 0.45 us per 64 of fp32, a
+//   x BN x 128), its loads (62 bytes a clock from L2 to an SM, 50 of each SM of
+//   a pair) and the issue of its instructions (0.22 us whatever BN is);
+//   an epilogue takes 0.6 us per 128 columns of bf16, 0.35 us per 64 of fp32, a
 //   sixth more where the tile cuts a piece of a row, five times that where C's
-//   rows are not aligned (2305 x 4999 x 129 in 128 columns: 23 us), and 90
+//   rows are not aligned (2305 x 4999 x 129 in 128 columns: 24 us), and 90
 //   clocks a column with the operands swapped, whose stores are narrow; it runs
-//   under the next tile's products;
+//   under the next tile's products, whose start it holds up where the
+//   accumulators overlap;
 //   starting and ending a kernel costs 2.6 us, a pair's cluster barriers and the
-//   turns of its tiles more than a single CTA's (4096 x 1536 x 768 in 192
-//   columns: 9.4 us single, 11.4 us paired; 16384 x 4096 x 8192 in 256 columns:
-//   333 and 291 us);
+//   turns of its tiles more (8192 x 8192 x 1024: 55 us in single CTAs of 224
+//   columns, 64 us in pairs of 256; 16384 x 4096 x 8192: 349 and 300 us);
 //   nothing is faster than its bytes from memory.
 Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
-  constexpr double kLoadRate = 56.0, kIssue = 430.0, kStart = 5200.0, kSwapColumn = 90.0, kJoin = 1500.0, kMemoryRate = 3300.0;
-  constexpr double kRoundF32 = 900.0, kRoundBf16 = 1600.0, kScalar = 5.0, kRagged = 1.15;
-  constexpr double kPair = 2000.0, kPairTurn = 2500.0, kTurn = 800.0, kSwapTurn = 5000.0;
+  constexpr double kLoadRate = 62.0, kPairLoadRate = 50.0, kIssue = 430.0, kStart = 5200.0, kSwapColumn = 90.0, kJoin = 1500.0, kMemoryRate = 3300.0;
+  constexpr double kRoundF32 = 700.0, kRoundBf16 = 1200.0, kScalar = 5.0, kRagged = 1.15;
+  constexpr double kPair = 2000.0, kPairTurn = 3000.0, kTurn = 300.0, kOverlapTurn = 1500.0, kSwapTurn = 5000.0;
   Choice ch = {1, false};
   double least = 1e300;
   const double memory = ((double)(a.M + a.N) * a.K + (double)a.M * a.N * (a.c_f32 ? 4 : 2)) / kMemoryRate;
@@ -564,12 +570,12 @@ Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
         if (ks > 1 && (!swap || ks > nkb || xt * yt * ks > room)) break;
         const int64_t ctas = xt * yt * ks * cg;
         const int64_t turns = ceil_div(ctas, per_sm * sms / cg * cg);
-        const double load = (kXRows + BN / cg) * 128 / kLoadRate * (ctas > sms ? per_sm : 1);
+        const double load = (kXRows + BN / cg) * 128 / (cg == 2 ? kPairLoadRate : kLoadRate) * (ctas > sms ? per_sm : 1);
         const int64_t rounds = ceil_div(ceil_div(BN, piece), 2);  // pieces of a row that each epilogue warp takes
         const double epilogue = swap ? kSwapColumn * BN : rounds * (a.c_f32 ? kRoundF32 : kRoundBf16) *
                                                               (a.c_vec ? 1.0 : kScalar) * (BN % piece ? kRagged : 1.0);
         const double main = ceil_div(nkb, ks) * fmax(fmax(2.0 * BN, load), kIssue);
-        const double path = turns * fmax(main, epilogue) + (cg == 2 ? turns * kPairTurn : swap ? (turns - 1) * kSwapTurn : turns * kTurn);
+        const double path = turns * fmax(main, epilogue) + (cg == 2 ? turns * kPairTurn : swap ? (turns - 1) * kSwapTurn : turns * (BN > 240 ? kOverlapTurn : kTurn));
         const double t = kStart + fmax(path, memory) + 0.1 * path + epilogue + (cg == 2 ? kPair : 0.0) + (ks > 1 ? kJoin : 0.0);
         if (t < least) {
           least = t;
