@@ -371,27 +371,23 @@ def _groups(n: int) -> int:
     return (n + Q8_GROUP - 1) // Q8_GROUP
 
 
-_NOTHING = contextlib.nullcontext()
-
-
 @contextlib.contextmanager
-def _on_stream(device, stream):
-    if stream is None:
-        with torch.cuda.device(device):
-            yield
-        return
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield
-
-
 def _on(device, stream):
     """The tensors' device and the caller's stream as the current ones, so that
     outputs and intermediates are allocated for the stream that uses them."""
-    if stream is None and (device if isinstance(device, int) else device.index) == torch.cuda.current_device():
-        return _NOTHING
-    return _on_stream(device, stream)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _elsewhere(dev, stream) -> bool:
+    """Whether a call for tensors on device `dev` (an index) has to go through _on."""
+    return stream is not None or dev != torch.cuda.current_device()
 
 
 def _same_device(*tensors):
@@ -436,9 +432,12 @@ def _q8_operand(name, t, scale):
 def forward_q8(desc: SpRsDesc, partials, residual, gamma, beta=None, stream=None, store_mask: bool = True) -> dict:
     """`forward` with the norm's output in e4m3: `q` [rows, H] and `scale`
     [rows, ceil(H/128)] in the place of `y`.  `backward` takes the rest."""
+    dev = _same_device(residual, gamma, beta, *partials)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return forward_q8(desc, partials, residual, gamma, beta, store_mask=store_mask)
     rows, H, T, ln = desc.rows, desc.H, desc.T, desc.norm == SP_LAYERNORM
     dt = residual.dtype
-    dev = _same_device(residual, gamma, beta, *partials)
     if DTYPE_CODE.get(dt) != desc.dtype or gamma.dtype != dt:
         raise ValueError("the tensors' types do not match the descriptor")
     if len(partials) != T or residual.numel() != rows * H or gamma.numel() != H:
@@ -449,18 +448,17 @@ def forward_q8(desc: SpRsDesc, partials, residual, gamma, beta=None, stream=None
             raise ValueError("the partials' types or sizes do not match the descriptor")
     if ln and (beta is None or beta.dtype != dt or beta.numel() != H):
         raise ValueError("LayerNorm needs beta, as gamma")
-    with _on(dev, stream):
-        cuda = residual.device
-        h = torch.empty((rows, H), device=cuda, dtype=dt)
-        q = q8_empty(rows, H, cuda, torch.float8_e4m3fn)
-        s = q8_empty(rows, _groups(H), cuda)
-        mask = torch.empty((rows, H), device=cuda, dtype=torch.uint8) if store_mask and desc.p > 0 else None
-        rstd = torch.empty(rows, device=cuda, dtype=torch.float32)
-        mean = torch.empty(rows, device=cuda, dtype=torch.float32) if ln else None
-        _check(lib().sp_rs_dropout_residual_norm_fwd_q8(
-            ctypes.byref(desc), (ctypes.c_void_p * T)(*[_ptr(p) for p in partials]), _ptr(residual), _ptr(gamma),
-            _ptr(beta), h.data_ptr(), q.data_ptr(), _ld16(H), s.data_ptr(), _ld16(_groups(H)), _ptr(mask),
-            rstd.data_ptr(), _ptr(mean), _stream(None)))
+    cuda, groups = residual.device, _groups(H)
+    h = torch.empty((rows, H), device=cuda, dtype=dt)
+    q = q8_empty(rows, H, cuda, torch.float8_e4m3fn)
+    s = q8_empty(rows, groups, cuda)
+    mask = torch.empty((rows, H), device=cuda, dtype=torch.uint8) if store_mask and desc.p > 0 else None
+    rstd = torch.empty(rows, device=cuda, dtype=torch.float32)
+    mean = torch.empty(rows, device=cuda, dtype=torch.float32) if ln else None
+    _check(lib().sp_rs_dropout_residual_norm_fwd_q8(
+        ctypes.byref(desc), (ctypes.c_void_p * T)(*[_ptr(p) for p in partials]), _ptr(residual), _ptr(gamma),
+        _ptr(beta), h.data_ptr(), q.data_ptr(), _ld16(H), s.data_ptr(), _ld16(groups), _ptr(mask),
+        rstd.data_ptr(), _ptr(mean), _stream(None)))
     return dict(h=h, q=q, scale=s, mask=mask, rstd=rstd, mean=mean)
 
 
@@ -476,6 +474,9 @@ def quantize_q8(x: torch.Tensor, fmt: str = "e4m3", block: bool = False, rowwise
     if not rowwise and not colwise:
         raise ValueError("neither rowwise nor colwise: nothing to do")
     dev = _same_device(x, scale)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return quantize_q8(x, fmt, block, rowwise, colwise, scale)
     M, K = x.shape
     ps, ldxs, srows = None, 0, 0
     if xcode >= 2:
@@ -487,18 +488,17 @@ def quantize_q8(x: torch.Tensor, fmt: str = "e4m3", block: bool = False, rowwise
     mg, kg = _groups(M), _groups(K)
     q = s = qt = st = pq = pqs = pqt = pqts = None
     ldq, ldqt = _ld16(K), _ld16(M)
-    with _on(dev, stream):
-        cuda = x.device
-        if rowwise:
-            q, s = q8_empty(M, K, cuda, out8), q8_empty(mg if block else M, kg, cuda)
-            pq, pqs = q.data_ptr(), s.data_ptr()
-        if colwise:
-            qt, st = q8_empty(K, M, cuda, out8), q8_empty(kg if block else K, mg, cuda)
-            pqt, pqts = qt.data_ptr(), st.data_ptr()
-        if M > 0 and K > 0:
-            d = SpQuantizeQ8Desc(M, K, ldx, ldxs, ldq, _ld16(kg), ldqt, _ld16(mg), xcode, ELEM_CODE[out8], srows,
-                                 1 if block else 0, 0)
-            _check(lib().sp_quantize_q8(ctypes.byref(d), px, ps, pq, pqs, pqt, pqts, _stream(None)))
+    cuda = x.device
+    if rowwise:
+        q, s = q8_empty(M, K, cuda, out8), q8_empty(mg if block else M, kg, cuda)
+        pq, pqs = q.data_ptr(), s.data_ptr()
+    if colwise:
+        qt, st = q8_empty(K, M, cuda, out8), q8_empty(kg if block else K, mg, cuda)
+        pqt, pqts = qt.data_ptr(), st.data_ptr()
+    if M > 0 and K > 0:
+        d = SpQuantizeQ8Desc(M, K, ldx, ldxs, ldq, _ld16(kg), ldqt, _ld16(mg), xcode, ELEM_CODE[out8], srows,
+                             1 if block else 0, 0)
+        _check(lib().sp_quantize_q8(ctypes.byref(d), px, ps, pq, pqs, pqt, pqts, _stream(None)))
     return dict(q=q, scale=s, qt=qt, scale_t=st)
 
 
@@ -510,25 +510,29 @@ def matmul_q8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: 
     counts), added to what a float32 `out` holds with `accumulate`."""
     if accumulate and out is None:
         raise ValueError("accumulate needs the out to add to")
-    dev = _same_device(a, a_scale, b, b_scale, out)
+    dev = _same_device(a, a_scale, b, b_scale, out, status)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return matmul_q8(a, a_scale, b, b_scale, out, out_dtype, accumulate, status=status)
     pa, lda, psa, ldas, asr = _q8_operand("a", a, a_scale)
     pb, ldb, psb, ldbs, bsr = _q8_operand("b", b, b_scale)
     (M, K), (N, Kb) = a.shape, b.shape
     if K != Kb:
         raise ValueError(f"a [M, K] and b [N, K] expected, got {tuple(a.shape)} and {tuple(b.shape)}")
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((M, N), device=a.device, dtype=out_dtype)
-        elif tuple(out.shape) != (M, N):
+    if out is None:
+        out = torch.empty((M, N), device=a.device, dtype=out_dtype)
+        pc, ldc = out.data_ptr(), N
+    else:
+        if tuple(out.shape) != (M, N):
             raise ValueError(f"out is {tuple(out.shape)}, the product {(M, N)}")
-        code = DTYPE_CODE.get(out.dtype)
-        if code is None:
-            raise ValueError("out: bfloat16 or float32 expected")
         pc, ldc = _rows2d(out)
-        if M > 0 and N > 0:
-            d = SpMatmulQ8Desc(M, N, K, lda, ldb, ldas, ldbs, ldc, _Q8_CODE[a.dtype], _Q8_CODE[b.dtype], code, asr, bsr,
-                               1 if accumulate else 0, _ptr(status))
-            _check(lib().sp_matmul_q8(ctypes.byref(d), pa, psa, pb, psb, pc, _stream(None)))
+    code = DTYPE_CODE.get(out.dtype)
+    if code is None:
+        raise ValueError("out: bfloat16 or float32 expected")
+    if M > 0 and N > 0:
+        d = SpMatmulQ8Desc(M, N, K, lda, ldb, ldas, ldbs, ldc, _Q8_CODE[a.dtype], _Q8_CODE[b.dtype], code, asr, bsr,
+                           1 if accumulate else 0, _ptr(status))
+        _check(lib().sp_matmul_q8(ctypes.byref(d), pa, psa, pb, psb, pc, _stream(None)))
     return out
 
 
@@ -540,11 +544,14 @@ def linear_q8_backward(dy: torch.Tensor, x_q: torch.Tensor, x_scale: torch.Tenso
     [M, K] is the forward's 8-bit input, wt_q [K, N] the transposed weight
     (quantize_q8's qt).  dy goes to 8 bits (`fmt`) along N for dx and along its
     tokens for dw, where x is requantised along its tokens too."""
-    with _on(dy.device, stream):
-        g = quantize_q8(dy, fmt, rowwise=True, colwise=True)
-        xt = quantize_q8(x_q, "e5m2" if x_q.dtype == torch.float8_e5m2 else "e4m3", rowwise=False, colwise=True,
-                         scale=x_scale)
-        dx = matmul_q8(g["q"], g["scale"], wt_q, wt_scale, out_dtype=dx_dtype)
-        dw = matmul_q8(g["qt"], g["scale_t"], xt["qt"], xt["scale_t"], out=dw, out_dtype=torch.float32,
-                       accumulate=dw is not None)
+    dev = _same_device(dy, x_q, x_scale, wt_q, wt_scale, dw)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return linear_q8_backward(dy, x_q, x_scale, wt_q, wt_scale, fmt, dw, dx_dtype)
+    g = quantize_q8(dy, fmt, rowwise=True, colwise=True)
+    xt = quantize_q8(x_q, "e5m2" if x_q.dtype == torch.float8_e5m2 else "e4m3", rowwise=False, colwise=True,
+                     scale=x_scale)
+    dx = matmul_q8(g["q"], g["scale"], wt_q, wt_scale, out_dtype=dx_dtype)
+    dw = matmul_q8(g["qt"], g["scale_t"], xt["qt"], xt["scale_t"], out=dw, out_dtype=torch.float32,
+                   accumulate=dw is not None)
     return dict(dx=dx, dw=dw)
