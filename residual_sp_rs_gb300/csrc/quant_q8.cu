@@ -288,14 +288,18 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
     }
     __syncthreads();
     // 16 bytes a lane: words 2j and 2j + 1 of column k, swapped where k / 8 is odd
-    const int j = threadIdx.x & 7;
+    // (for all of a thread's columns or none: they are 32 or 64 apart)
+    const int j = threadIdx.x & 7, k0 = threadIdx.x >> 3;
+    const int32_t row = (int32_t)tm * kQ8Group + 16 * j, cols = a.K - ((int32_t)tk * kQ8Group + k0);
+    const int32_t inside = a.M - row;  // bytes of the lane's 16 inside the tensor
+    uint8_t* out = a.qt + ((int64_t)tk * kQ8Group + k0) * a.ldqt + row;
+    const bool swapped = (k0 >> 3) & 1;
 #pragma unroll
-    for (int k = threadIdx.x >> 3; k < kQ8Group; k += kThreads / 8) {
-      const int32_t col = (int32_t)tk * kQ8Group + k, row = (int32_t)tm * kQ8Group + 16 * j;
-      const int kc = k >> 3;
-      uint4 u = reinterpret_cast<const uint4*>(tile)[k * 8 + (j ^ (kc >> 1))];
-      if (kc & 1) u = make_uint4(u.z, u.w, u.x, u.y);
-      if (col < a.K && row < a.M) store16(a.qt + (int64_t)col * a.ldqt + row, u, a.M - row);
+    for (int k = 0; k < kQ8Group; k += kThreads / 8) {
+      uint4 u = reinterpret_cast<const uint4*>(tile)[(k0 + k) * 8 + (j ^ ((k0 + k) >> 4))];
+      if (swapped) u = make_uint4(u.z, u.w, u.x, u.y);
+      if (k < cols && inside > 0) store16(out, u, inside);
+      out += (int64_t)(kThreads / 8) * a.ldqt;
     }
   }
 }

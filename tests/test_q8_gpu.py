@@ -142,6 +142,31 @@ def test_requantize_bits(M, K, src, block):
         assert same(r[name], want[0]) and same(r["scale" if name == "q" else "scale_t"], want[1])
 
 
+@pytest.mark.parametrize("spread,low", [(0, 120), (9, 110), (15, 40), (15, 186), (16, 100), (60, 60), (3, 2), (3, 250)])
+def test_requantize_over_scale_spreads(spread, low):
+    """Rows whose scales are near and far from each other, at both ends of the scale bytes, with zero rows and columns,
+    columns held only by the smallest scales, and a NaN."""
+    g = gen(spread * 300 + low)
+    M, K = 300, 270
+    bits = torch.randint(0, 256, (M, 272), generator=g, dtype=torch.uint8)
+    bits[(bits & 0x7F) == 0x7F] = 0x7E
+    bits[7], bits[:, 11] = 0, 0
+    bits[200:230, 20:40] = 0x01                    # the least subnormal
+    bits[:128, 50] = 0
+    bits[40, 50] = 0x81
+    s = torch.randint(low, low + spread + 1, (M, 16), generator=g).to(torch.uint8)
+    s[40] = low
+    s[41] = low + spread
+    if spread == 9:
+        bits[130, 200] = 0x7F
+    x, sc = bits.to(DEV)[:, :K].view(torch.float8_e4m3fn), s.to(DEV)[:, :3]
+    v = value(x, sc)
+    v = torch.where(v.abs() > torch.finfo(F32).max, math.inf, v)   # what fp32 cannot hold is not a number to it
+    r = ops.quantize_q8(x, "e4m3", rowwise=False, colwise=True, scale=sc)
+    want, byte = ref_quant(v.t().contiguous(), "e4m3")
+    assert same(r["scale_t"], byte) and same(r["qt"], want)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 def test_quantize_borders(fmt):
     """Groups of zeros, of the type's largest magnitudes and next to them, ties, fp32 subnormals and the largest fp32."""
