@@ -640,7 +640,7 @@ const char* sp_status_string(sp_status_t s) {
   }
 }
 
-int32_t sp_version(void) { return 300; }
+int32_t sp_version(void) { return 400; }
 
 #ifndef SPF_SOURCE_HASH
 #define SPF_SOURCE_HASH "unknown"

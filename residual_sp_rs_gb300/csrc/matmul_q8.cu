@@ -486,29 +486,28 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-cudaError_t encode_tiled(EncodeTiled* out) {
-  static void* fn = nullptr;  // the same pointer whoever looks it up
-  if (!fn) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
-    if (e != cudaSuccess) return e;
-    if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
-    fn = f;
-  }
-  *out = reinterpret_cast<EncodeTiled>(fn);
-  return cudaSuccess;
+struct Encoder {
+  EncodeTiled fn;
+  cudaError_t error;
+};
+
+Encoder find_encoder() {
+  void* f = nullptr;
+  cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+  const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+  if (e != cudaSuccess) return {nullptr, e};
+  if (found != cudaDriverEntryPointSuccess || !f) return {nullptr, cudaErrorNotSupported};
+  return {reinterpret_cast<EncodeTiled>(f), cudaSuccess};
 }
 
 }  // namespace
 
 cudaError_t byte_map(const void* p, int64_t rows, int64_t K, int64_t ld, int box, bool swizzle, CUtensorMap* map) {
-  EncodeTiled encode;
-  const cudaError_t e = encode_tiled(&encode);
-  if (e != cudaSuccess) return e;
+  static const Encoder encoder = find_encoder();  // once per process, whichever thread asks first
+  if (encoder.error != cudaSuccess) return encoder.error;
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
   const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, ones[2] = {1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, boxes, ones,
+  const CUresult r = encoder.fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, boxes, ones,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;

@@ -327,6 +327,27 @@ def test_matmul_nan_stays_in_its_row_and_column():
     assert same(got, want.double())
 
 
+def test_scales_in_torchs_exponent_type():
+    g = gen(8)
+    a, sa, av = exact8(g, 20, 300, "e4m3", False)
+    b, sb, bv = exact8(g, 30, 300, "e4m3", True)
+    e8 = torch.float8_e8m0fnu
+    assert same(ops.matmul_q8(a, sa.view(e8), b, sb.view(e8), out_dtype=F32), av @ bv.t())
+    x, y = (ops.quantize_q8(a, rowwise=False, colwise=True, scale=s) for s in (sa, sa.view(e8)))
+    assert torch.equal(x["qt"].view(torch.uint8), y["qt"].view(torch.uint8)) and torch.equal(x["scale_t"], y["scale_t"])
+
+
+def test_results_do_not_change_from_call_to_call():
+    """One token with K split in a cluster, single CTAs and pairs: the same sums in the same order every time."""
+    for M, N, K in ((1, 2048, 8192), (300, 500, 1024), (1000, 4100, 4200)):
+        g = torch.Generator(device=DEV).manual_seed(M)
+        a = ops.quantize_q8(torch.randn(M, K, device=DEV, generator=g))
+        b = ops.quantize_q8(torch.randn(N, K, device=DEV, generator=g), block=True)
+        want = ops.matmul_q8(a["q"], a["scale"], b["q"], b["scale"], out_dtype=F32)
+        for _ in range(10):
+            assert torch.equal(ops.matmul_q8(a["q"], a["scale"], b["q"], b["scale"], out_dtype=F32), want)
+
+
 def test_matmul_empty_sum_and_empty_sides():
     a, sa = ops.q8_empty(5, 0, DEV, torch.float8_e4m3fn), ops.q8_empty(5, 0, DEV)
     b, sb = ops.q8_empty(7, 0, DEV, torch.float8_e4m3fn), ops.q8_empty(7, 0, DEV)
