@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(512) sp_fwd_kernel(const FwdArgs a) {
     const int v = lr + k * tpr;
     if constexpr (Q8) {
       float yv[EV] = {};
-      uint32_t amax = 0u;
+      float amax = 0.f;
       if (v < a.nvec) {
         float gm[EV], hr[EV], bt[EV];
         V::unpack(sgb[v], gm);
@@ -190,12 +190,11 @@ __global__ void __launch_bounds__(512) sp_fwd_kernel(const FwdArgs a) {
           V::unpack(hp[k], hr);
         }
 #pragma unroll
-        for (int e = 0; e < EV; ++e) {
-          yv[e] = LN ? gm[e] * ((hr[e] - mu) * rstd) + bt[e] : gm[e] * (hr[e] * rstd);
-          amax = max(amax, abs_bits(yv[e]));
-        }
+        for (int e = 0; e < EV; ++e) yv[e] = LN ? gm[e] * ((hr[e] - mu) * rstd) + bt[e] : gm[e] * (hr[e] * rstd);
+#pragma unroll
+        for (int e = 0; e < EV; e += 2) amax = max3_abs(amax, yv[e], yv[e + 1]);
       }
-      const uint32_t sb = q8_scale_byte<false>(lanes_max<kQ8Group / EV>(amax));  // every lane takes part
+      const uint32_t sb = q8_scale_byte<false>(lanes_max<kQ8Group / EV>(__float_as_uint(amax)));  // every lane takes part
       if (v < a.nvec) {
         const float inv = q8_inv_scale(sb);
         uint32_t* yq = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(a.y) + r * a.ldq + (int64_t)v * EV);

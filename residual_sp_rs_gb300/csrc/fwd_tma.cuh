@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(NTHR, 1) sp_fwd_tma_kernel(const FwdArgs a, co
       const int v = lr + k * tpr;
       if constexpr (Q8) {
         f2_t yv[4] = {};
-        uint32_t amax = 0u;
+        float amax = 0.f;
         if (k < VPT - 1 || last_in) {
           const float4* gp = reinterpret_cast<const float4*>(sgb) + v;
 #pragma unroll
@@ -455,10 +455,10 @@ __global__ void __launch_bounds__(NTHR, 1) sp_fwd_tma_kernel(const FwdArgs a, co
           for (int q = 0; q < 4; ++q) {
             float lo, hi;
             f2_split(yv[q], lo, hi);
-            amax = max(amax, max(abs_bits(lo), abs_bits(hi)));
+            amax = max3_abs(amax, lo, hi);
           }
         }
-        const uint32_t sb = q8_scale_byte<false>(lanes_max<16>(amax));  // every lane takes part
+        const uint32_t sb = q8_scale_byte<false>(lanes_max<16>(__float_as_uint(amax)));  // every lane takes part
         if (k < VPT - 1 || last_in) {
           const float inv = q8_inv_scale(sb);
           const f2_t inv2 = f2(inv, inv);

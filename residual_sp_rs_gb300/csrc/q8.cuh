@@ -77,7 +77,12 @@ __device__ __forceinline__ void q8_unpack2(uint32_t w, bool e5m2, float& lo, flo
       : "r"(h2));
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// max(|a|, |b|, |c|), NaN when one is NaN.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // Largest of `v` over the LANES (a power of two) aligned neighbouring lanes.
 template <int LANES>

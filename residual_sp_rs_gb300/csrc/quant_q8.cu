@@ -39,13 +39,6 @@ struct Shape {
   static constexpr int kWords = S == Src::kBf16 ? 4 : 8;     // registers per row
 };
 
-// max(a, |b|, |c|) that keeps a NaN.
-__device__ __forceinline__ float max3_abs(float a, float b, float c) {
-  float r;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // Eight consecutive elements of a row from column `col` on, zero past K.
 template <Src S>
 __device__ __forceinline__ void load8(const QuantArgs& a, int32_t row, int32_t col, uint32_t (&w)[Shape<S>::kWords]) {
