@@ -593,6 +593,20 @@ def test_status_word_stays_clear():
     assert int(word) == 0
 
 
+def test_readme_example_runs():
+    """The 8-bit example, as written, behind the one before it."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(root, "README.md")).read(), flags=re.S)
+    names = {}
+    for block in blocks[:2]:
+        exec(compile(block, "README.md", "exec"), names)
+    torch.cuda.synchronize()
+    assert names["out"].shape == (4096, 1536) and names["lin"]["dw"].shape == (1536, 768)
+    assert all(bool(torch.isfinite(t.float()).all()) for t in (names["out"], names["lin"]["dx"], names["g"]["dgamma"]))
+
+
 # ---- bounded waits --------------------------------------------------------------------------------
 
 TIMEOUT_SHAPES = [(1300, 2600, 200), (1000, 4100, 4200), (9, 1000, 4096)]   # single CTAs, pairs, K split in a cluster
