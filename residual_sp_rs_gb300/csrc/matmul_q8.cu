@@ -526,7 +526,9 @@ struct Choice {
   bool swap;
 };
 
+// With the operands swapped: a short side leaves room for a second CTA on an SM.
 constexpr int kShortSide = 64;
+int ctas_per_sm(int BN) { return BN <= kShortSide ? 2 : 1; }
 
 int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
@@ -564,7 +566,7 @@ Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
       const int64_t xt = ceil_div(XR, (int64_t)kXRows * cg), yt = ceil_div(YR, BN);
       for (int ks = 1; ks <= 8; ks *= 2) {
         // of clusters of 2, 4 and 8 CTAs 152, 144 and 120 CTAs are resident at once on 152 SMs
-        const int per_sm = swap && BN <= kShortSide ? 2 : 1;
+        const int per_sm = swap ? ctas_per_sm(BN) : 1;
         const int64_t room = per_sm * (ks == 8 ? sms * 15 / 19 : ks == 4 ? sms * 18 / 19 : sms);
         if (ks > 1 && (!swap || ks > nkb || xt * yt * ks > room)) break;
         const int64_t ctas = xt * yt * ks * cg;
@@ -598,10 +600,8 @@ Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
   p.overlap = (int)p.acc1 < p.BN;  // BN 256: by 16 columns (or a split's one accumulator)
   const uint32_t stage = kXBytes + (uint32_t)(p.BN / ch.cg) * 128u;
   const uint32_t rest = 1024 + kScaleSlots * kScaleAtom * (1 + scale_atoms_y(p.BN)) + (ch.swap ? 0 : epilogue_warps(false) * kStoreBytes);
-  // 2048: the kernel's static shared memory and the driver's, rounded up.  A short side
-  // leaves half of an SM's shared memory to a second CTA: the split's, or the
-  // next kernel's, which then starts under this one's end.
-  const int64_t budget = (ch.swap && p.BN <= kShortSide ? optin / 2 : optin) - 2048;
+  // 2048: the kernel's static shared memory and the driver's, rounded up
+  const int64_t budget = (ch.swap ? optin / ctas_per_sm(p.BN) : optin) - 2048;
   int64_t stages = (budget - rest) / stage;
   if (stages > kMaxStages) stages = kMaxStages;
   const int64_t need = ceil_div(nkb, p.ks) * ceil_div((int64_t)p.xtiles * p.ytiles * p.ks * ch.cg, sms);
@@ -628,7 +628,8 @@ cudaError_t launch(const MatmulArgs& a, MatmulPlan p, int sms, cudaStream_t st) 
   const int64_t tiles = (int64_t)p.xtiles * p.ytiles;
   const int group = CG * p.ks;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.ks > 1 ? tiles : min(tiles, (int64_t)(sms / CG))) * group));
+  const int64_t resident = (int64_t)(SWAP ? ctas_per_sm(p.BN) : 1) * sms / CG;
+  cfg.gridDim = dim3((unsigned)((p.ks > 1 || tiles < resident ? tiles : resident) * group));
   cfg.blockDim = dim3(threads(SWAP));
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = st;
