@@ -8,9 +8,9 @@
 // A CTA takes a 128 x 128 tile, in which every group of either direction (and
 // a 128 x 128 block) is whole.  A thread holds the block of its kRows rows and
 // 8 columns in registers: bf16 as packed words, 8 rows; fp32 and 8-bit input as
-// fp32 values, 4 rows, so that 64 registers do and 32 warps fit on an SM.  A
-// row's maximum is then four shuffles over 16 lanes, a column's one shuffle and
-// a maximum over the warps in shared memory, and the bytes of a column's rows
+// fp32 values, 4 rows, so that 64 registers do and 32 warps fit on an SM.  The
+// rows' maxima are then taken over 16 lanes, a column's by one shuffle and
+// over the warps in shared memory, and the bytes of a column's rows
 // form one word of the transposed tile.  That tile goes through shared memory
 // (8-byte word r of column k at slot r ^ (k / 8), so that neither side meets a
 // bank conflict) and leaves 128 bytes of a column at a time.
@@ -38,6 +38,36 @@ struct Shape {
   static constexpr int kThreads = 16 * kQ8Group / kRows;
   static constexpr int kWords = S == Src::kBf16 ? 4 : 8;     // registers per row
 };
+
+// Maxima of R (4 or 8) rows over 16 lanes: at each step a lane hands over the
+// half of the rows that its partner keeps, so R + log2(16 / R) shuffles do
+// instead of 4 R, and what follows is worked out once per row instead of in 16
+// lanes.  The lane c of 16 ends up with row held_row(c), lane lane_of(r) has row r.
+template <int R>
+__device__ __forceinline__ uint32_t rows_max(uint32_t (&m)[R], int c) {
+#pragma unroll
+  for (int n = R / 2, off = 8; off > 0; n /= 2, off /= 2) {
+    if (n >= 1) {
+      const bool upper = c & off;
+#pragma unroll
+      for (int j = 0; j < n; ++j) {
+        const uint32_t keep = upper ? m[n + j] : m[j], send = upper ? m[j] : m[n + j];
+        m[j] = max(keep, __shfl_xor_sync(0xFFFFFFFFu, send, off));
+      }
+    } else {
+      m[0] = max(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], off));
+    }
+  }
+  return m[0];
+}
+template <int R>
+__device__ __forceinline__ constexpr int held_row(int c) {
+  return c / (16 / R);
+}
+template <int R>
+__device__ __forceinline__ constexpr int lane_of(int r) {
+  return r * (16 / R);
+}
 
 // Eight consecutive elements of a row from column `col` on, zero past K.
 template <Src S>
@@ -202,21 +232,28 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
       }
     }
     if (a.q) {
+      float inv = q8_inv_scale(bsb);  // without BLOCK that of row held_row(c)
+      if constexpr (!BLOCK) {
+        uint32_t m[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) m[i] = row_max(i);
+        const uint32_t sb = q8_scale_byte<E5M2>(rows_max<kRows>(m, c));
+        inv = q8_inv_scale(sb);
+        const int r = held_row<kRows>(c);
+        if (lane_of<kRows>(r) == c && r < rows) a.q_scale[(int64_t)(row0 + r) * a.ldq_scale + tk] = (uint8_t)sb;
+      }
+      uint8_t* out = a.q + (int64_t)row0 * a.ldq + col0;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        uint32_t sb = bsb;
-        if constexpr (!BLOCK) {
-          sb = q8_scale_byte<E5M2>(lanes_max<16>(row_max(i)));
-          if (c == 0 && i < rows) a.q_scale[(int64_t)(row0 + i) * a.ldq_scale + tk] = (uint8_t)sb;
-        }
-        if (i >= rows) continue;
-        const float inv = q8_inv_scale(sb);
-        const f2_t inv2 = f2(inv, inv);
+        const float f = BLOCK ? inv : __shfl_sync(0xFFFFFFFFu, inv, (lane & 16) + lane_of<kRows>(i));
+        const f2_t inv2 = f2(f, f);
         float e[8];
 #pragma unroll
         for (int p = 0; p < 4; ++p) f2_split(f2_mul(pair(i, p), inv2), e[2 * p], e[2 * p + 1]);
-        store8(a.q + (int64_t)(row0 + i) * a.ldq + col0,
-               make_uint2(q8_pack4<E5M2>(e[0], e[1], e[2], e[3]), q8_pack4<E5M2>(e[4], e[5], e[6], e[7])), a.K - col0);
+        if (i < rows)
+          store8(out, make_uint2(q8_pack4<E5M2>(e[0], e[1], e[2], e[3]), q8_pack4<E5M2>(e[4], e[5], e[6], e[7])),
+                 a.K - col0);
+        out += a.ldq;
       }
     }
     if (!a.qt) continue;
