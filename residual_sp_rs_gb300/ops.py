@@ -548,10 +548,44 @@ def linear_q8_backward(dy: torch.Tensor, x_q: torch.Tensor, x_scale: torch.Tenso
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return linear_q8_backward(dy, x_q, x_scale, wt_q, wt_scale, fmt, dw, dx_dtype)
-    g = quantize_q8(dy, fmt, rowwise=True, colwise=True)
-    xt = quantize_q8(x_q, "e5m2" if x_q.dtype == torch.float8_e5m2 else "e4m3", rowwise=False, colwise=True,
-                     scale=x_scale)
-    dx = matmul_q8(g["q"], g["scale"], wt_q, wt_scale, out_dtype=dx_dtype)
-    dw = matmul_q8(g["qt"], g["scale_t"], xt["qt"], xt["scale_t"], out=dw, out_dtype=torch.float32,
-                   accumulate=dw is not None)
+    q8, code = _Q8_CODE.get(Q8_DTYPE.get(fmt)), DTYPE_CODE.get(dy.dtype)
+    if len(dy.shape) != 2 or code is None or q8 is None:
+        raise ValueError("dy: a matrix of float32 or bfloat16 and a format e4m3 or e5m2 expected")
+    px, ldx, pxs, ldxs, xsr = _q8_operand("x_q", x_q, x_scale)
+    pw, ldw, pws, ldws, wsr = _q8_operand("wt_q", wt_q, wt_scale)
+    (M, N), K = dy.shape, x_q.shape[1]
+    if x_q.shape[0] != M or tuple(wt_q.shape) != (K, N):
+        raise ValueError(f"dy [M, N], x_q [M, K] and wt_q [K, N] expected, got {tuple(dy.shape)}, {tuple(x_q.shape)} "
+                         f"and {tuple(wt_q.shape)}")
+    if dx_dtype not in DTYPE_CODE:
+        raise ValueError("dx: bfloat16 or float32 expected")
+    accumulate, cuda = 0 if dw is None else 1, dy.device
+    if accumulate and (dw.dtype != torch.float32 or tuple(dw.shape) != (N, K)):
+        raise ValueError(f"dw: float32 of {(N, K)} expected, got {dw.dtype} of {tuple(dw.shape)}")
+    if M == 0 or N == 0 or K == 0:  # sums of nothing
+        return dict(dx=torch.zeros((M, K), device=cuda, dtype=dx_dtype),
+                    dw=torch.zeros((N, K), device=cuda, dtype=torch.float32) if dw is None else dw)
+    dx = torch.empty((M, K), device=cuda, dtype=dx_dtype)
+    if dw is None:
+        dw = torch.empty((N, K), device=cuda, dtype=torch.float32)
+    pdy, ldy = _rows2d(dy)
+    pdw, lddw = _rows2d(dw)
+    # dY in both directions and x^T, values and scales, in one buffer of the current stream
+    ldm, ldmg, ldn, ldng = _ld16(M), _ld16(_groups(M)), _ld16(N), _ld16(_groups(N))
+    buf = torch.empty(M * (ldn + ldng) + (N + K) * (ldm + ldmg), device=cuda, dtype=torch.uint8)
+    q = buf.data_ptr()
+    qs = q + M * ldn
+    qt = qs + M * ldng
+    qts = qt + N * ldm
+    xt = qts + N * ldmg
+    xts = xt + K * ldm
+    L, st, ref, xcode = lib(), _stream(None), ctypes.byref, _Q8_CODE[x_q.dtype]
+    _check(L.sp_quantize_q8(ref(SpQuantizeQ8Desc(M, N, ldy, 0, ldn, ldng, ldm, ldmg, code, q8, 0, 0, 0)),
+                            pdy, None, q, qs, qt, qts, st))
+    _check(L.sp_quantize_q8(ref(SpQuantizeQ8Desc(M, K, ldx, ldxs, 0, 0, ldm, ldmg, xcode, xcode, xsr, 0, 0)),
+                            px, pxs, None, None, xt, xts, st))
+    _check(L.sp_matmul_q8(ref(SpMatmulQ8Desc(M, K, N, ldn, ldw, ldng, ldws, K, q8, _Q8_CODE[wt_q.dtype],
+                                             DTYPE_CODE[dx_dtype], 1, wsr, 0, None)), q, qs, pw, pws, dx.data_ptr(), st))
+    _check(L.sp_matmul_q8(ref(SpMatmulQ8Desc(N, K, M, ldm, ldm, ldmg, ldmg, lddw, q8, xcode, 0, 1, 1, accumulate, None)),
+                          qt, qts, xt, xts, pdw, st))
     return dict(dx=dx, dw=dw)

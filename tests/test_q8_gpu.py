@@ -509,6 +509,33 @@ def test_training_step_together():
     assert bool(torch.isfinite(b["d_res"].float()).all() and torch.isfinite(b["dgamma"]).all())
 
 
+@pytest.mark.parametrize("M,N,K,dtype,fmt,block", [(1, 16, 16, BF16, "e4m3", True), (77, 95, 361, BF16, "e5m2", True),
+                                                   (300, 129, 264, F32, "e4m3", False)])
+def test_linear_backward_is_its_parts(M, N, K, dtype, fmt, block):
+    """The same bits as the quantisations and products called one by one; dw added to what is given; no rows."""
+    g = gen(M + N + K)
+    dy = randn(g, M, N, std=1e-3).to(dtype).to(DEV)
+    x = ops.quantize_q8(randn(g, M, K).to(DEV))
+    w = ops.quantize_q8(randn(g, N, K).to(DEV), block=block, colwise=True)
+    got = ops.linear_q8_backward(dy, x["q"], x["scale"], w["qt"], w["scale_t"], fmt)
+    d = ops.quantize_q8(dy, fmt, colwise=True)
+    xt = ops.quantize_q8(x["q"], rowwise=False, colwise=True, scale=x["scale"])
+    assert torch.equal(got["dx"], ops.matmul_q8(d["q"], d["scale"], w["qt"], w["scale_t"]))
+    dw = ops.matmul_q8(d["qt"], d["scale_t"], xt["qt"], xt["scale_t"], out_dtype=F32)
+    assert torch.equal(got["dw"], dw)
+    base = randn(g, N, K + 2).to(DEV)
+    total = base.clone()
+    more = ops.linear_q8_backward(dy, x["q"], x["scale"], w["qt"], w["scale_t"], fmt, dw=total[:, 1:K + 1], dx_dtype=F32)
+    assert more["dx"].dtype == F32 and torch.equal(total[:, 1:K + 1], base[:, 1:K + 1] + dw)
+    assert torch.equal(total[:, 0], base[:, 0]) and torch.equal(total[:, K + 1], base[:, K + 1])
+    none = ops.linear_q8_backward(dy[:0], x["q"][:0], x["scale"][:0], w["qt"], w["scale_t"], fmt, dw=total[:, 1:K + 1])
+    assert none["dx"].shape == (0, K) and torch.equal(total[:, 1:K + 1], base[:, 1:K + 1] + dw)
+    for bad in (dict(dy=dy[:, :N - 1]), dict(fmt="e3m4"), dict(dw=total), dict(dx_dtype=torch.float16)):
+        args = dict(dict(dy=dy, x_q=x["q"], x_scale=x["scale"], wt_q=w["qt"], wt_scale=w["scale_t"], fmt=fmt), **bad)
+        with pytest.raises(ValueError):
+            ops.linear_q8_backward(**args)
+
+
 def test_gradient_against_differences():
     """dx and dw are the gradients of L = sum(dy * (x W^T)), linear in x and in W: differences of the 8-bit forward
     product itself, with steps that 8 bits hold exactly."""
