@@ -174,7 +174,8 @@ sp_status_t sp_rs_dropout_residual_norm_fwd_rows(const sp_rs_desc_t* desc,
  * columns and either one row per row of the tensor or, for a tensor
  * quantised in 128 x 128 blocks, one row per 128 rows.  Values and scales
  * have row strides in bytes that are multiples of 16 and 16-byte aligned
- * bases; what lies between the end of a row and its stride is neither read
+ * bases (multiples of 128 bytes are faster: no row then straddles cache
+ * lines); what lies between the end of a row and its stride is neither read
  * as a value nor written.
  * Quantising a group: s is the smallest integer with max|x| <= 448 * 2^s
  * (e4m3) or 57344 * 2^s (e5m2), at least -127; byte = s + 127 and

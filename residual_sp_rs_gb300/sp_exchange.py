@@ -68,7 +68,8 @@ def forward_from_shard_rows(desc, blocks: torch.Tensor, residual, gamma, beta, h
                             mask_out, rstd_out, mean_out, stream=None) -> None:
     """The fused forward of shard desc.j from its rows of each partial:
     blocks [T, R, H] as returned by exchange_partials (contiguous, each
-    block 16-byte aligned)."""
+    block 16-byte aligned).  y_out: the norm's output, or a pair (q, scale)
+    for it in 8 bits."""
     T, R, H = blocks.shape
     if desc.T != T or desc.H != H or desc.R != R or max(1, desc.nshards) != 1:
         raise ValueError("blocks do not match the descriptor's single shard")
@@ -76,8 +77,12 @@ def forward_from_shard_rows(desc, blocks: torch.Tensor, residual, gamma, beta, h
         raise ValueError("blocks must be contiguous: each block is passed by its base address")
     row_bytes = H * blocks.element_size()
     base = [blocks[t].data_ptr() - desc.j * R * row_bytes for t in range(T)]
-    ops.sp_rs_dropout_residual_norm_fwd(desc, base, residual, gamma, beta, h_out, y_out, mask_out,
-                                        rstd_out, mean_out, stream)
+    if isinstance(y_out, tuple):
+        ops.sp_rs_dropout_residual_norm_fwd_q8(desc, base, residual, gamma, beta, h_out, *y_out, mask_out,
+                                               rstd_out, mean_out, stream)
+    else:
+        ops.sp_rs_dropout_residual_norm_fwd(desc, base, residual, gamma, beta, h_out, y_out, mask_out,
+                                            rstd_out, mean_out, stream)
 
 
 def allreduce_norm_grads(dgamma: torch.Tensor, dbeta: torch.Tensor | None = None, group=None) -> None:
@@ -159,7 +164,8 @@ def forward_pipelined(desc, partial: torch.Tensor, residual, gamma, beta, h_out,
                       rstd_out, mean_out, chunks: int = 4, group=None):
     """The fused forward of this rank's shard (desc.j = rank, desc.T = world
     size, one shard) from every rank's full partial, the exchange pipelined
-    in chunks.  The kernels go to the current stream, which each chunk's
+    in chunks.  y_out: the norm's output, or a pair (q, scale) for it in 8
+    bits.  The kernels go to the current stream, which each chunk's
     transfers are ordered with.  Returns the chunk receive buffers: keep them
     alive until the forward has run."""
     T = dist.get_world_size(group)
@@ -174,9 +180,13 @@ def forward_pipelined(desc, partial: torch.Tensor, residual, gamma, beta, h_out,
     for (b, e), buf, ws in zip(bounds, recv, works):
         for w in ws:
             w.wait()
-        ops.sp_rs_dropout_residual_norm_fwd_rows(desc, b, e - b, chunk_partial_bases(own, buf, j, R, b),
-                                                 residual, gamma, beta, h_out, y_out, mask_out, rstd_out,
-                                                 mean_out)
+        bases = chunk_partial_bases(own, buf, j, R, b)
+        if isinstance(y_out, tuple):
+            ops.sp_rs_dropout_residual_norm_fwd_q8_rows(desc, b, e - b, bases, residual, gamma, beta, h_out, *y_out,
+                                                        mask_out, rstd_out, mean_out)
+        else:
+            ops.sp_rs_dropout_residual_norm_fwd_rows(desc, b, e - b, bases, residual, gamma, beta, h_out, y_out,
+                                                     mask_out, rstd_out, mean_out)
     return recv
 
 
@@ -190,7 +200,7 @@ def gather_q8(q: torch.Tensor, scale: torch.Tensor, group=None):
     out = []
     for t in (q, scale):
         R, C = t.shape
-        ld = ops._ld16(C)
+        ld = ops._q8_ld(C)
         if t.is_contiguous() and ld == C:
             rows = t.view(torch.uint8)
         else:  # whole 16-byte rows travel

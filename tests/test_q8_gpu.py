@@ -620,6 +620,36 @@ def test_status_word_stays_clear():
     assert int(word) == 0
 
 
+def test_pipelined_forward_and_gather_on_one_nccl_rank():
+    """The exchange's forwards with an 8-bit y, and its gather, give the plain call's bits (T = 1)."""
+    import socket
+
+    import torch.distributed as dist
+
+    from residual_sp_rs_gb300 import sp_exchange as ex
+    with socket.socket() as sk:
+        sk.bind(("127.0.0.1", 0))
+        port = sk.getsockname()[1]
+    dist.init_process_group("nccl", init_method=f"tcp://127.0.0.1:{port}", rank=0, world_size=1)
+    try:
+        desc, parts, res, gamma, _ = region(1, 200, 2, 264, "bf16", "rms", 0.1, 4)
+        want = ops.forward_q8(desc, parts, res, gamma)
+        for pipelined in (True, False):
+            out = {k: torch.zeros_like(v) for k, v in want.items() if v is not None and k not in ("q", "scale")}
+            q, s = ops.q8_empty(desc.rows, 264, DEV, torch.float8_e4m3fn), ops.q8_empty(desc.rows, 3, DEV)
+            if pipelined:
+                ex.forward_pipelined(desc, parts[0], res, gamma, None, out["h"], (q, s), out["mask"], out["rstd"], None)
+            else:
+                ex.forward_from_shard_rows(desc, parts[0].view(1, -1, 264), res, gamma, None, out["h"], (q, s),
+                                           out["mask"], out["rstd"], None)
+            fq, fs = ex.gather_q8(q, s)
+            torch.cuda.synchronize()
+            assert all(torch.equal(out[k], want[k]) for k in out)
+            assert torch.equal(fq.view(torch.uint8), want["q"].view(torch.uint8)) and torch.equal(fs, want["scale"])
+    finally:
+        dist.destroy_process_group()
+
+
 def test_readme_example_runs():
     """The 8-bit example, as written, behind the one before it."""
     import os
