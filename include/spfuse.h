@@ -459,6 +459,33 @@ typedef struct sp_plan_info_t {
 sp_status_t sp_plan_describe(const sp_rs_desc_t* desc, int32_t sms, int32_t smem_optin,
                              int32_t has_dh, int32_t has_mask, sp_plan_info_t* out);
 
+/* The launch configuration of one sp_matmul_q8 call.  X is the operand whose
+ * rows fill the tensor core's 128 lanes (A, or B when swapped), Y the other. */
+typedef struct sp_matmul_q8_plan_t {
+  int32_t pair;           /* 1: pairs of CTAs work on tiles of 256 rows of X, 0: single CTAs, 128 rows */
+  int32_t swapped;        /* 1: X is B (few rows of A) */
+  int32_t bn;             /* rows of Y per tile */
+  int32_t split_k;        /* CTAs of a cluster that split K */
+  int32_t stages;         /* ring stages, 128 bytes of K of a CTA's rows each */
+  int32_t block;          /* threads per CTA */
+  int32_t tmem_cols;      /* tensor memory columns allocated per CTA */
+  int32_t acc1_col;       /* first column of the second accumulator (the first is at 0) */
+  int32_t scale_col;      /* first column of the scales */
+  int32_t ctas_per_sm;    /* CTAs an SM holds at a time */
+  int64_t stage_bytes;    /* one ring stage */
+  int64_t smem_bytes;     /* dynamic shared memory per CTA */
+  int64_t tiles;          /* tiles of C */
+  int64_t ctas;           /* grid size */
+} sp_matmul_q8_plan_t;
+
+/* What sp_matmul_q8 would launch for `desc` on a device with `sms`
+ * multiprocessors and `smem_optin` bytes of opt-in shared memory per block,
+ * with C 16-byte aligned; all zero where M or N is 0 and nothing is launched.
+ * Host arithmetic only.  Errors: the descriptor's, SP_ERR_INVALID_ARG for a
+ * NULL `out`, non-positive limits or too little shared memory for the tile. */
+sp_status_t sp_matmul_q8_plan(const sp_matmul_q8_desc_t* desc, int32_t sms, int32_t smem_optin,
+                              sp_matmul_q8_plan_t* out);
+
 #ifdef __cplusplus
 }
 #endif

@@ -422,6 +422,52 @@ sp_status_t bwd_impl(const sp_rs_desc_t* desc, bool ranged, int64_t row_begin, i
 }
 
 
+// Checks the product's descriptor (not the pointers).
+sp_status_t check_matmul(const sp_matmul_q8_desc_t* d) {
+  if (!d) return SP_ERR_INVALID_ARG;
+  for (const int32_t t : {d->a_dtype, d->b_dtype})
+    if (t != SP_ELEM_E4M3 && t != SP_ELEM_E5M2) return SP_ERR_DTYPE;
+  if (d->c_dtype != SP_ELEM_F32 && d->c_dtype != SP_ELEM_BF16) return SP_ERR_DTYPE;
+  for (const int32_t r : {d->a_scale_rows, d->b_scale_rows})
+    if (r != 1 && r != kQ8Group) return SP_ERR_INVALID_ARG;
+  if (d->accumulate != 0 && d->accumulate != 1) return SP_ERR_INVALID_ARG;
+  if (d->accumulate && d->c_dtype != SP_ELEM_F32) return SP_ERR_DTYPE;  // sums are kept in fp32
+  if (!aligned(d->status, 4)) return SP_ERR_ALIGN;
+  if (d->M < 0 || d->N < 0 || d->K < 0 || d->M >= kMaxQ8Dim || d->N >= kMaxQ8Dim || d->K >= kMaxQ8Dim)
+    return SP_ERR_SHAPE;
+  if (q8_groups(d->M) * ((d->N + 15) / 16) >= kMaxQ8Dim || q8_groups(d->N) * ((d->M + 15) / 16) >= kMaxQ8Dim)
+    return SP_ERR_SHAPE;  // tiles of C
+  const int64_t am = d->a_scale_rows == 1 ? d->M : q8_groups(d->M), bn = d->b_scale_rows == 1 ? d->N : q8_groups(d->N);
+  if (!q8_strides_ok(d->M, d->K, d->lda, am, d->lda_scale) || !q8_strides_ok(d->N, d->K, d->ldb, bn, d->ldb_scale))
+    return SP_ERR_SHAPE;
+  if (d->ldc < d->N || (d->M > 0 && d->ldc > ((int64_t)1 << 58) / d->M)) return SP_ERR_SHAPE;
+  return SP_OK;
+}
+
+// The product's arguments but for the pointers, C taken as 16-byte aligned.
+MatmulArgs matmul_args(const sp_matmul_q8_desc_t& d) {
+  MatmulArgs m = {};
+  m.M = d.M;
+  m.N = d.N;
+  m.K = d.K;
+  m.lda = d.lda;
+  m.ldb = d.ldb;
+  m.ldc = d.ldc;
+  m.lda_scale = d.lda_scale;
+  m.ldb_scale = d.ldb_scale;
+  m.a_scale_rows = d.a_scale_rows;
+  m.b_scale_rows = d.b_scale_rows;
+  m.a_e5m2 = d.a_dtype == SP_ELEM_E5M2;
+  m.b_e5m2 = d.b_dtype == SP_ELEM_E5M2;
+  m.c_f32 = d.c_dtype == SP_ELEM_F32;
+  m.c_vec = d.ldc * (m.c_f32 ? 4 : 2) % 16 == 0;
+  m.accumulate = d.accumulate;
+  m.status = d.status;
+  m.wait_ns = wait_hooks().wait_ns;
+  m.drop_stage = wait_hooks().drop_stage;
+  return m;
+}
+
 }  // namespace
 }  // namespace spf
 
@@ -519,53 +565,20 @@ sp_status_t sp_quantize_q8(const sp_quantize_q8_desc_t* d, const void* x, const 
 
 sp_status_t sp_matmul_q8(const sp_matmul_q8_desc_t* d, const uint8_t* a, const uint8_t* a_scale,
                          const uint8_t* b, const uint8_t* b_scale, void* c, sp_stream_t stream) {
-  if (!d) return SP_ERR_INVALID_ARG;
-  for (const int32_t t : {d->a_dtype, d->b_dtype})
-    if (t != SP_ELEM_E4M3 && t != SP_ELEM_E5M2) return SP_ERR_DTYPE;
-  if (d->c_dtype != SP_ELEM_F32 && d->c_dtype != SP_ELEM_BF16) return SP_ERR_DTYPE;
-  for (const int32_t r : {d->a_scale_rows, d->b_scale_rows})
-    if (r != 1 && r != kQ8Group) return SP_ERR_INVALID_ARG;
-  if (d->accumulate != 0 && d->accumulate != 1) return SP_ERR_INVALID_ARG;
-  if (d->accumulate && d->c_dtype != SP_ELEM_F32) return SP_ERR_DTYPE;  // sums are kept in fp32
-  if (!aligned(d->status, 4)) return SP_ERR_ALIGN;
-  if (d->M < 0 || d->N < 0 || d->K < 0 || d->M >= kMaxQ8Dim || d->N >= kMaxQ8Dim || d->K >= kMaxQ8Dim)
-    return SP_ERR_SHAPE;
-  if (q8_groups(d->M) * ((d->N + 15) / 16) >= kMaxQ8Dim || q8_groups(d->N) * ((d->M + 15) / 16) >= kMaxQ8Dim)
-    return SP_ERR_SHAPE;  // tiles of C
-  const int64_t am = d->a_scale_rows == 1 ? d->M : q8_groups(d->M), bn = d->b_scale_rows == 1 ? d->N : q8_groups(d->N);
-  if (!q8_strides_ok(d->M, d->K, d->lda, am, d->lda_scale) || !q8_strides_ok(d->N, d->K, d->ldb, bn, d->ldb_scale))
-    return SP_ERR_SHAPE;
-  if (d->ldc < d->N || (d->M > 0 && d->ldc > ((int64_t)1 << 58) / d->M)) return SP_ERR_SHAPE;
+  const sp_status_t st = check_matmul(d);
+  if (st != SP_OK) return st;
   if (d->M == 0 || d->N == 0) return SP_OK;  // nothing to write
   if (!c || (d->K > 0 && (!a || !a_scale || !b || !b_scale))) return SP_ERR_INVALID_ARG;
   if (!aligned(a, 16) || !aligned(a_scale, 16) || !aligned(b, 16) || !aligned(b_scale, 16) ||
       !aligned(c, d->c_dtype == SP_ELEM_F32 ? 4 : 2))
     return SP_ERR_ALIGN;
-  MatmulArgs m = {};
+  MatmulArgs m = matmul_args(*d);
   m.a = a;
   m.a_scale = a_scale;
   m.b = b;
   m.b_scale = b_scale;
   m.c = c;
-  m.M = d->M;
-  m.N = d->N;
-  m.K = d->K;
-  m.lda = d->lda;
-  m.ldb = d->ldb;
-  m.ldc = d->ldc;
-  m.lda_scale = d->lda_scale;
-  m.ldb_scale = d->ldb_scale;
-  m.a_scale_rows = d->a_scale_rows;
-  m.b_scale_rows = d->b_scale_rows;
-  m.a_e5m2 = d->a_dtype == SP_ELEM_E5M2;
-  m.b_e5m2 = d->b_dtype == SP_ELEM_E5M2;
-  m.c_f32 = d->c_dtype == SP_ELEM_F32;
-  const int64_t cb = m.c_f32 ? 4 : 2;
-  m.c_vec = aligned(c, 16) && d->ldc * cb % 16 == 0;
-  m.accumulate = d->accumulate;
-  m.status = d->status;
-  m.wait_ns = wait_hooks().wait_ns;
-  m.drop_stage = wait_hooks().drop_stage;
+  m.c_vec = m.c_vec && aligned(c, 16);
   if (inject_launch_failure()) return SP_ERR_CUDA;
   return from_cuda(launch_matmul_q8(m, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -692,6 +705,22 @@ sp_status_t sp_plan_describe(const sp_rs_desc_t* desc, int32_t sms, int32_t smem
     b.ctas = bp.ctas;
     b.workspace_bytes = (int64_t)bp.ws_bytes;
     b.noalloc_fits = noalloc_scratch_fits(bp.ws_bytes) ? 1 : 0;
+  }
+  return SP_OK;
+}
+
+sp_status_t sp_matmul_q8_plan(const sp_matmul_q8_desc_t* desc, int32_t sms, int32_t smem_optin,
+                              sp_matmul_q8_plan_t* out) {
+  const sp_status_t st = check_matmul(desc);
+  if (st != SP_OK) return st;
+  if (!out || sms < 1 || smem_optin < 1) return SP_ERR_INVALID_ARG;
+  std::memset(out, 0, sizeof(*out));
+  if (desc->M == 0 || desc->N == 0) return SP_OK;  // nothing is launched
+  describe_matmul_q8(matmul_args(*desc), sms, smem_optin, out);
+  // a ring of two stages and, with K split, the fp32 sums in the ring's place
+  if (out->stages < 2 || (out->split_k > 1 && out->stages * out->stage_bytes < (int64_t)out->bn * 512)) {
+    std::memset(out, 0, sizeof(*out));
+    return SP_ERR_INVALID_ARG;
   }
   return SP_OK;
 }

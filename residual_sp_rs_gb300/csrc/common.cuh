@@ -295,7 +295,8 @@ __device__ __forceinline__ uint32_t residual_bf2(f2_t res, f2_t acc, f2_t s_hi, 
 // second rounding can only differ from the single one above where E is within
 // half an fp32 step of a bf16 midpoint, so h is off by at most 1/2 + 2^-16
 // bf16 steps: behind a norm that goes on to 8 bits the exact tie decision
-// would cost a quarter more instructions and buy nothing.
+// would buy nothing, and this takes fewer instructions and no second mode for
+// dyadic scales.
 // With c the bf16 truncation of fl(res + acc*s_hi), res - c is exact (8-bit
 // significands; the exponents are close unless the sum cancels), so t is E - c
 // to 2^-32 of E and c + t is E rounded to fp32.  Where the sum cancels or is

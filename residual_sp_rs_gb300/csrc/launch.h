@@ -126,6 +126,7 @@ cudaError_t byte_map(const void* p, int64_t rows, int64_t K, int64_t ld, int box
 // x_dtype: sp_elem_t; the rest of the shape is in the arguments.
 cudaError_t launch_quant_q8(const QuantArgs& a, int x_dtype, bool e5m2, bool block, cudaStream_t st);
 cudaError_t launch_matmul_q8(const MatmulArgs& a, cudaStream_t st);
+void describe_matmul_q8(const MatmulArgs& a, int sms, int optin, sp_matmul_q8_plan_t* out);
 
 cudaError_t launch_layout(bool to_hp, const void* in, void* out, int64_t N, int64_t H, int32_t T,
                           int elem_bytes, cudaStream_t stream);

@@ -24,6 +24,14 @@
 // sums through distributed shared memory in rank order, so the result does not
 // depend on timing.
 //
+// Bounds and what was measured (back to back): a large product by the tensor
+// core's power (16384 x 4096 x 8192: 316-325 us, 3.4 PFLOP/s; 291 us on zeros) and
+// by the 64 KB a pair and block of K that come from L2 (the same loop without
+// loads: 259 us); few tokens by the weights' bytes from memory (1 x 32768 x 8192:
+// 42 us, 95% of the copy bandwidth; 1 x 8192 x 8192: 14 us, 71%, of which 3.4 us
+// start and join); small products by starting, the first copies' latency and the
+// last epilogue (4096 x 1536 x 768: 8.7 us).
+//
 // Every wait is bounded (tma.cuh); a role that gives up reports it in the
 // status word, the tiles that were not finished are written as NaN, and tensor
 // memory is freed after the instructions and copies in flight are done.
@@ -559,6 +567,7 @@ Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
   for (int mode = 0; mode < 3; ++mode) {  // one CTA, a pair of CTAs, one CTA with the operands swapped
     const int cg = mode == 1 ? 2 : 1;
     const bool swap = mode == 2;
+    if (cg > sms) continue;
     const int64_t XR = swap ? a.N : a.M, YR = swap ? a.M : a.N;
     for (int BN = 256; BN >= 16; BN -= 16) {
       if (cg == 2 && BN % 32 != 0) continue;
@@ -613,6 +622,12 @@ Choice choose_plan(const MatmulArgs& a, int sms, int optin, MatmulPlan* best) {
   return ch;
 }
 
+// A CTA (pair, cluster) per tile, or as many as are resident at once.
+int64_t grid_of(const MatmulPlan& p, const Choice& ch, int sms) {
+  const int64_t tiles = (int64_t)p.xtiles * p.ytiles, resident = (int64_t)(ch.swap ? ctas_per_sm(p.BN) : 1) * sms / ch.cg;
+  return (p.ks > 1 || tiles < resident ? tiles : resident) * ch.cg * p.ks;
+}
+
 template <int CG, bool SWAP>
 cudaError_t launch(const MatmulArgs& a, MatmulPlan p, int sms, cudaStream_t st) {
   CUtensorMap mx = {}, my = {};
@@ -625,11 +640,9 @@ cudaError_t launch(const MatmulArgs& a, MatmulPlan p, int sms, cudaStream_t st) 
   auto k = sp_matmul_q8_kernel<CG, SWAP>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)p.xtiles * p.ytiles;
   const int group = CG * p.ks;
   cudaLaunchConfig_t cfg = {};
-  const int64_t resident = (int64_t)(SWAP ? ctas_per_sm(p.BN) : 1) * sms / CG;
-  cfg.gridDim = dim3((unsigned)((p.ks > 1 || tiles < resident ? tiles : resident) * group));
+  cfg.gridDim = dim3((unsigned)grid_of(p, {CG, SWAP}, sms));
   cfg.blockDim = dim3(threads(SWAP));
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = st;
@@ -645,6 +658,25 @@ cudaError_t launch(const MatmulArgs& a, MatmulPlan p, int sms, cudaStream_t st) 
 }
 
 }  // namespace
+
+void describe_matmul_q8(const MatmulArgs& a, int sms, int optin, sp_matmul_q8_plan_t* out) {
+  MatmulPlan p = {};
+  const Choice ch = choose_plan(a, sms, optin, &p);
+  out->pair = ch.cg == 2 ? 1 : 0;
+  out->swapped = ch.swap ? 1 : 0;
+  out->bn = p.BN;
+  out->split_k = p.ks;
+  out->stages = p.stages;
+  out->block = threads(ch.swap);
+  out->tmem_cols = (int32_t)p.tmem_cols;
+  out->acc1_col = (int32_t)p.acc1;
+  out->scale_col = (int32_t)p.sf_col;
+  out->ctas_per_sm = ch.swap ? ctas_per_sm(p.BN) : 1;
+  out->stage_bytes = kXBytes + (int64_t)(p.BN / ch.cg) * 128;
+  out->smem_bytes = p.smem;
+  out->tiles = (int64_t)p.xtiles * p.ytiles;
+  out->ctas = grid_of(p, ch, sms);
+}
 
 cudaError_t launch_matmul_q8(const MatmulArgs& a, cudaStream_t st) {
   int dev = 0, sms = 0, optin = 0;

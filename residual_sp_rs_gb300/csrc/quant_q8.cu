@@ -18,6 +18,11 @@
 // An 8-bit tile is 16 KB, too little for the resident CTAs to keep the memory
 // busy between their barriers.  So two CTAs stay on each SM, and tiled bulk
 // copies bring the next kRing tiles of each while one is worked on.
+//
+// 66 M values: bf16 along the rows 32.5 us (90% of the copy bandwidth), along
+// the columns 36 (81%), both 47 (82%); 8-bit along the rows 29 us (67%), along
+// the columns 35 (56%: 13 instructions a value and four barriers a tile);
+// 33.5 M fp32 values in blocks, both ways, 35 us (84%).
 #include "common.cuh"
 #include "launch.h"
 #include "q8.cuh"

@@ -84,6 +84,13 @@ class SpMatmulQ8Desc(ctypes.Structure):
                                               "accumulate")] + [("status", ctypes.c_void_p)]
 
 
+class SpMatmulQ8Plan(ctypes.Structure):
+    """Mirror of sp_matmul_q8_plan_t (include/spfuse.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("pair", "swapped", "bn", "split_k", "stages", "block", "tmem_cols",
+                                              "acc1_col", "scale_col", "ctas_per_sm")] + \
+               [(n, ctypes.c_int64) for n in ("stage_bytes", "smem_bytes", "tiles", "ctas")]
+
+
 def make_desc(T, j, S, B, H, dtype="bf16", norm="rms", p=0.0, eps=1e-6, seed=0, nshards=1,
               status=None):
     """status: an int32/uint32 CUDA tensor of one element (the device status
@@ -132,6 +139,8 @@ def lib() -> ctypes.CDLL:
         L.sp_quantize_q8.argtypes = [ctypes.POINTER(SpQuantizeQ8Desc), vp, vp, vp, vp, vp, vp, vp]
         L.sp_matmul_q8.restype = ctypes.c_int
         L.sp_matmul_q8.argtypes = [ctypes.POINTER(SpMatmulQ8Desc), vp, vp, vp, vp, vp, vp]
+        L.sp_matmul_q8_plan.restype = ctypes.c_int
+        L.sp_matmul_q8_plan.argtypes = [ctypes.POINTER(SpMatmulQ8Desc), i32, i32, ctypes.POINTER(SpMatmulQ8Plan)]
         for name in ("sp2hp", "hp2sp"):
             f = getattr(L, name)
             f.restype = ctypes.c_int
@@ -298,6 +307,15 @@ def sp_matmul_q8(desc: SpMatmulQ8Desc, a, a_scale, b, b_scale, c, stream=None) -
     """Pointers or tensors; the strides are the descriptor's."""
     _check(lib().sp_matmul_q8(ctypes.byref(desc), _addr(a), _addr(a_scale), _addr(b), _addr(b_scale), _addr(c),
                               _stream(stream)))
+
+
+def sp_matmul_q8_plan(desc: SpMatmulQ8Desc, sms: int, smem_optin: int) -> dict:
+    """The launch configuration of the product `desc` on a device with `sms`
+    multiprocessors and `smem_optin` bytes of opt-in shared memory per block;
+    host arithmetic only (no GPU needed)."""
+    info = SpMatmulQ8Plan()
+    _check(lib().sp_matmul_q8_plan(ctypes.byref(desc), int(sms), int(smem_optin), ctypes.byref(info)))
+    return {n: getattr(info, n) for n, _ in SpMatmulQ8Plan._fields_}
 
 
 # ---- conveniences that allocate outputs ------------------------------------------

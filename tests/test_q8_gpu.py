@@ -272,7 +272,7 @@ def test_matmul_exact_sums(M, N, K, af, bf, ablock, bblock):
 @pytest.mark.parametrize("M,N,K", [(1300, 2600, 200), (4000, 1500, 256), (2305, 4999, 129), (4096, 4104, 384),
                                    (9000, 520, 1100), (2304, 4096, 4200), (2300, 4099, 4200), (1000, 4100, 4200)])
 def test_matmul_exact_sums_many_tiles(M, N, K):
-    """Several tiles per CTA or (the longer K) CTA pair, ragged on every side."""
+    """Several tiles per CTA (2304 x 4096 x 4200: per CTA pair), ragged on every side."""
     g = gen(M + N)
     a, sa, av = exact8(g, M, K, "e4m3", False)
     b, sb, bv = exact8(g, N, K, "e4m3", True)
@@ -282,6 +282,34 @@ def test_matmul_exact_sums_many_tiles(M, N, K):
     assert same(ops.matmul_q8(a, sa, b, sb), want.float().to(BF16).double())
     c = torch.ones(M, N, device=DEV)
     assert same(ops.matmul_q8(a, sa, b, sb, out=c, accumulate=True), want + 1)
+
+
+def plan_of(M, N, K, out_dtype=F32):
+    """What the product launches on this device."""
+    ld, lds = (K + 15) // 16 * 16, ((K + 127) // 128 + 15) // 16 * 16
+    d = ops.SpMatmulQ8Desc(M, N, K, ld, ld, lds, lds, N, 2, 2, 0 if out_dtype == F32 else 1, 1, 1, 0, None)
+    props = torch.cuda.get_device_properties(0)
+    return ops.sp_matmul_q8_plan(d, props.multi_processor_count, getattr(props, "shared_memory_per_block_optin", 232448))
+
+
+# CTA pairs: one and several tiles each, with accumulators that overlap (256 columns) and not, ragged on every side
+PAIRS = [(4097, 1001, 4200), (2047, 2050, 4201), (4000, 2050, 4200), (3001, 4099, 4200)]
+
+
+@pytest.mark.parametrize("M,N,K", PAIRS)
+@pytest.mark.parametrize("af,bf,ablock,bblock", [("e4m3", "e4m3", False, True), ("e5m2", "e4m3", True, False)])
+def test_matmul_exact_sums_pairs(M, N, K, af, bf, ablock, bblock):
+    assert plan_of(M, N, K)["pair"] and plan_of(M, N, K, BF16)["pair"]
+    g = gen(M + 3 * N)
+    a, sa, av = exact8(g, M, K, af, ablock)
+    b, sb, bv = exact8(g, N, K, bf, bblock)
+    want = (av.to(DEV) @ bv.to(DEV).t()).cpu()
+    assert float(want.abs().max()) < 2.0 ** 24
+    assert same(ops.matmul_q8(a, sa, b, sb, out_dtype=F32), want)
+    assert same(ops.matmul_q8(a, sa, b, sb), want.float().to(BF16).double())
+    c = torch.full((M, N + 3), 1.0, device=DEV)
+    assert same(ops.matmul_q8(a, sa, b, sb, out=c[:, :N], accumulate=True), want + 1)
+    assert bool((c[:, N:] == 1).all())
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 256, 4096), (3, 72, 8192), (31, 130, 1000), (130, 300, 2048), (512, 384, 1024)])
@@ -339,7 +367,8 @@ def test_scales_in_torchs_exponent_type():
 
 def test_results_do_not_change_from_call_to_call():
     """One token with K split in a cluster, single CTAs and pairs: the same sums in the same order every time."""
-    for M, N, K in ((1, 2048, 8192), (300, 500, 1024), (1000, 4100, 4200)):
+    assert plan_of(1, 2048, 8192)["split_k"] > 1 and not plan_of(1000, 4100, 4200)["pair"] and plan_of(*PAIRS[3])["pair"]
+    for M, N, K in ((1, 2048, 8192), (300, 500, 1024), (1000, 4100, 4200), PAIRS[3]):
         g = torch.Generator(device=DEV).manual_seed(M)
         a = ops.quantize_q8(torch.randn(M, K, device=DEV, generator=g))
         b = ops.quantize_q8(torch.randn(N, K, device=DEV, generator=g), block=True)
@@ -666,7 +695,7 @@ def test_readme_example_runs():
 
 # ---- bounded waits --------------------------------------------------------------------------------
 
-TIMEOUT_SHAPES = [(1300, 2600, 200), (1000, 4100, 4200), (9, 1000, 4096)]   # single CTAs, pairs, K split in a cluster
+TIMEOUT_SHAPES = [(1300, 2600, 200), (1000, 4100, 4200), (9, 1000, 4096), PAIRS[1]]   # single CTAs twice, K split, pairs
 
 
 def _timeout_child(path):
@@ -690,6 +719,7 @@ def test_timed_out_wait_marks_its_tiles_and_sets_the_status_word(tmp_path):
     import sys
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     path = str(tmp_path / "child.pt")
+    assert [(p["pair"], p["split_k"] > 1) for p in (plan_of(*s) for s in TIMEOUT_SHAPES)] == [(0, False), (0, False), (0, True), (1, False)]
     env = dict(os.environ, SPFUSE_TEST_WAIT_NS="2000000", SPFUSE_TEST_DROP_STAGE="1")
     code = f"import sys; sys.path.insert(0, {root!r}); from tests.test_q8_gpu import _timeout_child; _timeout_child({path!r})"
     r = subprocess.run([sys.executable, "-c", code], env=env, cwd=root, capture_output=True, text=True, timeout=300)

@@ -176,6 +176,91 @@ def test_q8_empty_strides(spf):
         assert t.shape == (3, cols) and t.stride(0) % 16 == 0 and t.stride(0) >= cols
 
 
+# ---- what the product launches -----------------------------------------------------------
+
+def _plan(spf, M, N, K, c_dtype=1, sms=152, optin=232448, ldc=None):
+    ld, lds = (K + 15) // 16 * 16, ((K + 127) // 128 + 15) // 16 * 16
+    d = spf.SpMatmulQ8Desc(M, N, K, ld, ld, lds, lds, N if ldc is None else ldc, 2, 2, c_dtype, 1, 1, 0, None)
+    return spf.sp_matmul_q8_plan(d, sms, optin)
+
+
+SIDES = (1, 16, 33, 64, 65, 128, 300, 768, 1000, 1536, 2049, 4096, 8192, 16384, 40000)
+
+
+@pytest.mark.parametrize("M", SIDES)
+def test_matmul_plans_fit_the_device(spf, M):
+    """Shared memory, tensor memory, the ring, the join and the grid over sides and depths."""
+    for N in SIDES:
+        for K in (0, 1, 128, 129, 512, 768, 2048, 4200, 8192, 30000):
+            for c_dtype, sms, optin in ((1, 152, 232448), (0, 152, 232448), (0, 148, 232448), (1, 16, 232448)):
+                p = _plan(spf, M, N, K, c_dtype, sms, optin)
+                what = (M, N, K, c_dtype, sms, p)
+                cg, X, Y = 1 + p["pair"], (N if p["swapped"] else M), (M if p["swapped"] else N)
+                nkb = -(-K // 128)
+                assert 16 <= p["bn"] <= 256 and p["bn"] % (16 * cg) == 0, what
+                assert p["tiles"] == -(-X // (128 * cg)) * -(-Y // p["bn"]), what
+                # shared memory: the ring, the scales' ring, the epilogue's pieces, alignment and static arrays
+                rest = 1024 + 4 * 512 * (1 + -(-p["bn"] // 128)) + (0 if p["swapped"] else 8 * 4096)
+                assert p["stage_bytes"] == 128 * (128 + p["bn"] // cg) and p["smem_bytes"] == rest + p["stages"] * p["stage_bytes"], what
+                assert 2 <= p["stages"] <= 12 and (p["smem_bytes"] + 2048) * p["ctas_per_sm"] <= optin, what
+                # tensor memory: two accumulators (sharing less than a piece of columns; one when K is split), then the scales
+                assert p["tmem_cols"] in (32, 64, 128, 256, 512) and p["tmem_cols"] * p["ctas_per_sm"] <= 512, what
+                assert p["scale_col"] % 16 == 0 and p["scale_col"] + 4 + 4 * -(-p["bn"] // 128) <= p["tmem_cols"], what
+                assert p["bn"] <= p["scale_col"], what
+                if p["split_k"] == 1:
+                    assert p["acc1_col"] >= p["bn"] - 16 and p["acc1_col"] + p["bn"] <= p["scale_col"], what
+                else:
+                    assert p["swapped"] and p["split_k"] in (2, 4, 8) and p["split_k"] <= nkb, what
+                    assert p["bn"] * 512 <= p["stages"] * p["stage_bytes"], what     # the fp32 sums take the ring's place
+                    assert p["ctas"] == p["tiles"] * p["split_k"] <= p["ctas_per_sm"] * sms, what
+                assert p["ctas"] % (cg * p["split_k"]) == 0 and p["ctas"] <= max(p["ctas_per_sm"] * sms, cg), what
+                assert p["block"] == (256 if p["swapped"] else 384), what
+
+
+def test_matmul_plans_of_known_shapes(spf):
+    one = _plan(spf, 1, 8192, 8192)
+    assert one["swapped"] and one["bn"] == 16 and one["split_k"] == 4 and one["ctas_per_sm"] == 2
+    large = _plan(spf, 16384, 4096, 8192)
+    assert large["pair"] and large["bn"] == 256 and large["ctas"] == 152
+    pages = _plan(spf, 4096, 1536, 768)
+    # the estimate, in clocks: 2 turns of tiles 176 wide 5200 + 1.1 * (2 * 6 * 304 * 128 / 62 + 600) + 2 * 1200 * 1.15 = 16904,
+    # 192 wide 5200 + 1.1 * (2 * 6 * 320 * 128 / 62 + 600) + 2 * 1200 = 16981
+    assert not pages["pair"] and not pages["swapped"] and pages["bn"] == 176
+
+    # the shapes that the GPU tests count on: pairs with one and with several tiles each, accumulators that overlap
+    # (256 columns) and not, ragged on every side
+    for M, N, K, pair, swapped, split, turns in ((1300, 2600, 200, 0, 0, 0, 2), (1000, 4100, 4200, 0, 0, 0, 1),
+                                                 (9, 1000, 4096, 0, 1, 1, 1), (2304, 4096, 4200, 1, 0, 0, 2),
+                                                 (4097, 1001, 4200, 1, 0, 0, 1), (2047, 2050, 4201, 1, 0, 0, 1),
+                                                 (4000, 2050, 4200, 1, 0, 0, 2), (3001, 4099, 4200, 1, 0, 0, 3)):
+        for c_dtype in (0, 1):
+            p = _plan(spf, M, N, K, c_dtype)
+            got = (p["pair"], p["swapped"], int(p["split_k"] > 1))
+            assert got == (pair, swapped, split), (M, N, K, p)
+            assert -(-p["tiles"] * (1 + p["pair"]) * p["split_k"] // p["ctas"]) >= turns, (M, N, K, p)
+    assert _plan(spf, 4000, 2050, 4200)["bn"] == 256 and _plan(spf, 3001, 4099, 4200)["bn"] < 256
+
+
+def test_matmul_plan_refusals(spf):
+    info = spf.SpMatmulQ8Plan()
+    assert ctypes.sizeof(info) == 72
+    d = spf.SpMatmulQ8Desc(5, 7, 200, 208, 208, 16, 16, 7, 2, 3, 1, 1, 128, 0, None)
+    L = spf.lib()
+    assert L.sp_matmul_q8_plan(ctypes.byref(d), 152, 232448, ctypes.byref(info)) == 0 and info.tiles > 0
+    assert L.sp_matmul_q8_plan(ctypes.byref(d), 0, 232448, ctypes.byref(info)) == 1
+    assert L.sp_matmul_q8_plan(ctypes.byref(d), 152, 232448, None) == 1
+    for optin in (1, 2048, 20000):   # no room for two stages
+        assert L.sp_matmul_q8_plan(ctypes.byref(d), 152, optin, ctypes.byref(info)) == 1
+    big = spf.SpMatmulQ8Desc(16384, 4096, 8192, 8192, 8192, 64, 64, 4096, 2, 2, 1, 1, 1, 0, None)
+    for sms in (1, 2, 3):            # a pair needs two
+        assert L.sp_matmul_q8_plan(ctypes.byref(big), sms, 232448, ctypes.byref(info)) == 0
+        assert info.ctas <= sms and not (sms == 1 and info.pair)
+    d.lda = 200
+    assert L.sp_matmul_q8_plan(ctypes.byref(d), 152, 232448, ctypes.byref(info)) == 2
+    d.lda, d.M = 208, 0
+    assert L.sp_matmul_q8_plan(ctypes.byref(d), 152, 232448, ctypes.byref(info)) == 0 and info.tiles == 0
+
+
 # ---- the gather across ranks -----------------------------------------------------------
 
 def _gather_rank(rank, world, port, out, R, H):
