@@ -558,6 +558,8 @@ sp_status_t sp_quantize_q8(const sp_quantize_q8_desc_t* d, const void* x, const 
   a.tiles = mg * kg;
   a.x_scale_shift = d->x_scale_rows == kQ8Group ? 7 : 0;
   a.vec = aligned(x, 16) && d->ldx * xb % 16 == 0;
+  a.wait_ns = wait_hooks().wait_ns;
+  a.drop_stage = wait_hooks().drop_stage;
   if (inject_launch_failure()) return SP_ERR_CUDA;
   return from_cuda(launch_quant_q8(a, d->x_dtype, d->q_dtype == SP_ELEM_E5M2, d->block != 0,
                                    reinterpret_cast<cudaStream_t>(stream)));

@@ -505,6 +505,8 @@ struct QuantArgs {
   int64_t tiles;            // 128 x 128 tiles
   int32_t x_scale_shift;    // 8-bit x: row r has its scales in row r >> this
   int32_t vec;              // x allows aligned vector loads
+  int32_t drop_stage;       // test hook: CTA 0 never copies this one of its 8-bit tiles (-1: none)
+  uint64_t wait_ns;         // bound of every mbarrier wait
 };
 
 struct MatmulArgs {

@@ -17,7 +17,9 @@
 //
 // An 8-bit tile is 16 KB, too little for the resident CTAs to keep the memory
 // busy between their barriers.  So two CTAs stay on each SM, and tiled bulk
-// copies bring the next kRing tiles of each while one is worked on.
+// copies bring the next kRing tiles of each while one is worked on.  Waits for
+// them are bounded; a CTA whose wait runs out takes its tiles by plain loads
+// from there on, so that only time is lost.
 //
 // 66 M values: bf16 along the rows 32.5 us (90% of the copy bandwidth), along
 // the columns 36 (81%), both 47 (82%); 8-bit along the rows 29 us (67%), along
@@ -101,6 +103,17 @@ __device__ __forceinline__ void load8(const QuantArgs& a, int32_t row, int32_t c
   }
 }
 
+// Eight consecutive bytes of a row of an 8-bit x, zero past K.
+__device__ __forceinline__ uint2 load8_q8(const QuantArgs& a, int32_t row, int32_t col) {
+  const uint8_t* p = static_cast<const uint8_t*>(a.x) + (int64_t)row * a.ldx + col;
+  if (a.K - col >= 8) return *reinterpret_cast<const uint2*>(p);
+  uint32_t w[2] = {};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < a.K - col) w[e / 4] |= (uint32_t)p[e] << (8 * (e & 3));
+  return make_uint2(w[0], w[1]);
+}
+
 // Up to N (8 or 16) bytes to p, `n` of them inside the tensor.
 __device__ __forceinline__ void store8(uint8_t* p, uint2 w, int32_t n) {
   if (n >= 8) {
@@ -132,6 +145,7 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
   extern __shared__ __align__(128) unsigned char ring_raw[];
   unsigned char* const ring = ring_raw + ((128u - (smem_addr(ring_raw) & 127u)) & 127u);
   __shared__ uint64_t landed[kRing];
+  __shared__ uint32_t open_tile, open_stage, open_phase;  // thread 0's: where a wait ran out
   if constexpr (S == Src::kQ8) {
     if (threadIdx.x == 0) {
       prefetch_tensor_map(&map);
@@ -146,6 +160,7 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
   // 8-bit x: tile `t` to stage `s` of the ring
   auto fetch = [&](uint32_t t, int s) {
     if (t >= (uint32_t)a.tiles) return;
+    if (blockIdx.x == 0 && a.drop_stage >= 0 && t == (uint32_t)a.drop_stage * gridDim.x) return;  // test hook: never lands
     const uint32_t tm = t / (uint32_t)a.ktiles, tk = t - tm * (uint32_t)a.ktiles;
     mbar_arrive_expect_tx(&landed[s], kTileBytes);
     tma_load_2d<1>(smem_addr(ring) + s * kTileBytes, &map, (int32_t)(tk * kQ8Group), (int32_t)(tm * kQ8Group),
@@ -156,6 +171,7 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
       for (int s = 0; s < kRing; ++s) fetch(blockIdx.x + s * gridDim.x, s);
   int stage = 0;
   uint32_t phase = 0;
+  bool copies = true;  // no wait of this CTA has run out
 
   // tiles, rows and columns stay below 2^31; a.tiles + kRing * gridDim.x below 2^32
   for (uint32_t t = blockIdx.x; t < (uint32_t)a.tiles; t += gridDim.x) {
@@ -168,18 +184,33 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
       if (c < kRows && c < rows)
         xs = a.x_scale[(int64_t)((row0 + c) >> a.x_scale_shift) * a.ldx_scale + tk];
     if constexpr (S == Src::kQ8) {
-      const bool ok = mbar_wait(&landed[stage], phase, kWaitNs);
+      const bool was = copies, ok = was && mbar_wait(&landed[stage], phase, a.wait_ns);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {  // what never landed goes on as NaN
+      for (int i = 0; i < kRows; ++i) {
         const uint2 u = *reinterpret_cast<const uint2*>(ring + stage * kTileBytes + (kRows * g + i) * 128 + 8 * c);
-        w[i][0] = ok ? u.x : 0x7F7F7F7Fu;
-        w[i][1] = ok ? u.y : 0x7F7F7F7Fu;
+        w[i][0] = u.x;
+        w[i][1] = u.y;
       }
-      __syncthreads();  // the stage, and the last tile's words and maxima, have been read
-      if (threadIdx.x == 0) fetch(t + kRing * gridDim.x, stage);
-      if (++stage == kRing) {
-        stage = 0;
-        phase ^= 1u;
+      copies = __syncthreads_and(ok);  // and the stage, and the last tile's words and maxima, have been read
+      if (copies) {
+        if (threadIdx.x == 0) fetch(t + kRing * gridDim.x, stage);
+        if (++stage == kRing) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      } else {
+        // no copy is started any more, least of all on the barriers whose phases are open
+        if (was && threadIdx.x == 0) {
+          open_tile = t;
+          open_stage = stage;
+          open_phase = phase;
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const uint2 u = i < rows ? load8_q8(a, row0 + i, col0) : make_uint2(0u, 0u);
+          w[i][0] = u.x;
+          w[i][1] = u.y;
+        }
       }
     } else {
 #pragma unroll
@@ -337,6 +368,19 @@ __global__ void __launch_bounds__(Shape<S>::kThreads, 1024 / Shape<S>::kThreads)
       out += (int64_t)(kThreads / 8) * a.ldqt;
     }
   }
+  // None of the copies under way may land when the CTA has left.  (After the
+  // loop: this second wait inside it cost the loop 5%.)
+  if constexpr (S == Src::kQ8)
+    if (!copies && threadIdx.x == 0) {
+      uint32_t s = open_stage, p = open_phase;
+      for (uint32_t t = open_tile, n = 0; n < kRing && t < (uint32_t)a.tiles; ++n, t += gridDim.x) {
+        mbar_wait(&landed[s], p, a.wait_ns);
+        if (++s == kRing) {
+          s = 0;
+          p ^= 1u;
+        }
+      }
+    }
 }
 
 template <Src S, bool XE5M2 = false>
