@@ -465,6 +465,11 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
   // ---- the cluster's sums over K, in rank order ------------------------------------
   if (CG == 2) {
     cluster_sync();
+    // The commits arrive at the barriers of both CTAs.  The leader has waited
+    // for the last one of its own; the other CTA's may still be on its way (a
+    // cluster barrier orders threads, not these), and has to find its barrier.
+    if (warp == 1 && !leader) mbar_wait_cluster(&sh.drain, 0, limit);
+    __syncwarp();
   } else if (p.ks > 1) {
     cluster_sync();  // one tile per cluster: every CTA's part is in its shared memory
     if constexpr (SWAP) {

@@ -76,3 +76,47 @@ def test_requantisation_goes_on_without_its_copies(tmp_path, stage):
         for name in want:
             assert (got[name] is None) == (want[name] is None), name
             assert want[name] is None or torch.equal(got[name], want[name]), (M, K, name)
+
+
+# ---- products in a row ----------------------------------------------------------------------
+
+def plan_of(M, N, K, out_dtype=torch.float32, ldc=None):
+    """What the product launches on this device."""
+    ld, lds = (K + 15) // 16 * 16, ((K + 127) // 128 + 15) // 16 * 16
+    d = ops.SpMatmulQ8Desc(M, N, K, ld, ld, lds, lds, N if ldc is None else ldc, 2, 2, 0 if out_dtype == torch.float32 else 1,
+                           1, 1, 0, None)
+    props = torch.cuda.get_device_properties(0)
+    return ops.sp_matmul_q8_plan(d, props.multi_processor_count, getattr(props, "shared_memory_per_block_optin", 232448))
+
+
+def operand(R, C, seed):
+    """Whole numbers -3..3 in e4m3 with scales 1 and 2: fp32 holds the sums of their products.  Values, scales, float64."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    whole = torch.randint(-3, 4, (R, C), generator=g, device=DEV)
+    q, s = ops.q8_empty(R, C, DEV), ops.q8_empty(R, -(-C // 128), DEV)
+    q.copy_(whole.float().to(torch.float8_e4m3fn).view(torch.uint8))
+    s.copy_(torch.randint(127, 129, s.shape, generator=g, device=DEV))
+    v = whole.double() * (s.double() - 126).repeat_interleave(128, 1)[:, :C]   # 2^0 and 2^1
+    return q.view(torch.float8_e4m3fn), s, v
+
+
+def test_kernels_in_a_row_behind_pairs():
+    """The next kernel starts while the last CTAs of a pair leave: pairs behind pairs, a quantisation and a split
+    product behind pairs, each launch with the bits that it has alone."""
+    shapes = [(2047, 2050, 512), (1, 2048, 4096), (2047, 2050, 4201)]
+    assert plan_of(*shapes[2])["pair"] and plan_of(*shapes[1])["split_k"] > 1
+    ins = [(operand(M, K, M), operand(N, K, N)) for M, N, K in shapes]
+    want = [a[2] @ b[2].t() for a, b in ins]
+    x = ins[2][0]
+    quant = ops.quantize_q8(x[0], scale=x[1], colwise=True)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        outs = []
+        for i in (2, 2, 1, 2, 0, 2):
+            (a, sa, _), (b, sb, _) = ins[i]
+            outs.append((i, ops.matmul_q8(a, sa, b, sb, out_dtype=torch.float32)))
+            if i == 2:
+                q = ops.quantize_q8(x[0], scale=x[1], colwise=True)
+        for i, c in outs:
+            assert torch.equal(c.double(), want[i])
+        assert all(torch.equal(bits(q[k]), bits(quant[k])) for k in quant)
