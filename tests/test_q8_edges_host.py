@@ -9,6 +9,8 @@ def spf():
     return ops
 
 
-def test_smoke_runs_a_product_in_pairs(spf):
+def test_smoke_runs_pairs_and_a_split_product(spf):
     import __graft_entry__ as entry
-    assert spf.sp_matmul_q8_plan(entry.pairs_desc(spf), 152, 232448)["pair"] == 1
+    assert spf.sp_matmul_q8_plan(entry.product_desc(spf, *entry.PAIRS), 152, 232448)["pair"] == 1
+    assert spf.sp_matmul_q8_plan(entry.product_desc(spf, *entry.SPLIT), 152, 232448)["split_k"] > 1
+    assert entry.SPLIT[1:] == entry.PAIRS[1:]   # the same operands, a few rows of A
