@@ -527,7 +527,9 @@ def matmul_q8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: 
               stream=None, status=None) -> torch.Tensor:
     """a [M, K] times b [N, K] transposed, both 8-bit tensors, to [M, N] of
     `out_dtype` (bfloat16 or float32); into `out` when given (its type then
-    counts), added to what a float32 `out` holds with `accumulate`."""
+    counts), added to what a float32 `out` holds with `accumulate`.  `status`:
+    the device status word (as in `make_desc`) that a wait that ran out is
+    reported in; the tiles that it left unfinished are NaN."""
     if accumulate and out is None:
         raise ValueError("accumulate needs the out to add to")
     dev = _same_device(a, a_scale, b, b_scale, out, status)
@@ -558,16 +560,17 @@ def matmul_q8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: 
 
 def linear_q8_backward(dy: torch.Tensor, x_q: torch.Tensor, x_scale: torch.Tensor, wt_q: torch.Tensor,
                        wt_scale: torch.Tensor, fmt: str = "e4m3", dw: torch.Tensor | None = None,
-                       dx_dtype=torch.bfloat16, stream=None) -> dict:
+                       dx_dtype=torch.bfloat16, stream=None, status=None) -> dict:
     """Gradients of y = x W^T from dy [M, N] (float32 or bfloat16): `dx` [M, K]
     = dy W and `dw` [N, K] = dy^T x (float32; added to the given `dw`).  x_q
     [M, K] is the forward's 8-bit input, wt_q [K, N] the transposed weight
     (quantize_q8's qt).  dy goes to 8 bits (`fmt`) along N for dx and along its
-    tokens for dw, where x is requantised along its tokens too."""
-    dev = _same_device(dy, x_q, x_scale, wt_q, wt_scale, dw)
+    tokens for dw, where x is requantised along its tokens too.  A product whose
+    wait runs out reports it in the `status` word, as `matmul_q8` does."""
+    dev = _same_device(dy, x_q, x_scale, wt_q, wt_scale, dw, status)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
-            return linear_q8_backward(dy, x_q, x_scale, wt_q, wt_scale, fmt, dw, dx_dtype)
+            return linear_q8_backward(dy, x_q, x_scale, wt_q, wt_scale, fmt, dw, dx_dtype, status=status)
     q8, code = _Q8_CODE.get(Q8_DTYPE.get(fmt)), DTYPE_CODE.get(dy.dtype)
     if len(dy.shape) != 2 or code is None or q8 is None:
         raise ValueError("dy: a matrix of float32 or bfloat16 and a format e4m3 or e5m2 expected")
@@ -599,13 +602,13 @@ def linear_q8_backward(dy: torch.Tensor, x_q: torch.Tensor, x_scale: torch.Tenso
         total += (n + 127) // 128 * 128
     buf = torch.empty(total, device=cuda, dtype=torch.uint8)
     q, qs, qt, qts, xt, xts = [buf.data_ptr() + n for n in at]
-    L, st, ref, xcode = lib(), _stream(None), ctypes.byref, _Q8_CODE[x_q.dtype]
+    L, st, ref, xcode, word = lib(), _stream(None), ctypes.byref, _Q8_CODE[x_q.dtype], _ptr(status)
     _check(L.sp_quantize_q8(ref(SpQuantizeQ8Desc(M, N, ldy, 0, ldn, ldng, ldm, ldmg, code, q8, 0, 0, 0)),
                             pdy, None, q, qs, qt, qts, st))
     _check(L.sp_quantize_q8(ref(SpQuantizeQ8Desc(M, K, ldx, ldxs, 0, 0, ldm, ldmg, xcode, xcode, xsr, 0, 0)),
                             px, pxs, None, None, xt, xts, st))
     _check(L.sp_matmul_q8(ref(SpMatmulQ8Desc(M, K, N, ldn, ldw, ldng, ldws, K, q8, _Q8_CODE[wt_q.dtype],
-                                             DTYPE_CODE[dx_dtype], 1, wsr, 0, None)), q, qs, pw, pws, dx.data_ptr(), st))
-    _check(L.sp_matmul_q8(ref(SpMatmulQ8Desc(N, K, M, ldm, ldm, ldmg, ldmg, lddw, q8, xcode, 0, 1, 1, accumulate, None)),
+                                             DTYPE_CODE[dx_dtype], 1, wsr, 0, word)), q, qs, pw, pws, dx.data_ptr(), st))
+    _check(L.sp_matmul_q8(ref(SpMatmulQ8Desc(N, K, M, ldm, ldm, ldmg, ldmg, lddw, q8, xcode, 0, 1, 1, accumulate, word)),
                           qt, qts, xt, xts, pdw, st))
     return dict(dx=dx, dw=dw)

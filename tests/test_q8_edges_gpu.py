@@ -120,3 +120,50 @@ def test_kernels_in_a_row_behind_pairs():
         for i, c in outs:
             assert torch.equal(c.double(), want[i])
         assert all(torch.equal(bits(q[k]), bits(quant[k])) for k in quant)
+
+
+# ---- the status word of the gradients ------------------------------------------------------
+
+def gradients(word):
+    """dY in e4m3 and x of whole numbers, 1300 x 700 x 600; dw added to ones."""
+    x, sx, _ = operand(1300, 600, 1)
+    wt, swt, _ = operand(600, 700, 2)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    dy = torch.randint(-3, 4, (1300, 700), generator=g, device=DEV).float()
+    dw = torch.ones(700, 600, device=DEV)
+    r = ops.linear_q8_backward(dy, x, sx, wt, swt, dw=dw, dx_dtype=torch.float32, status=word)
+    torch.cuda.synchronize()
+    return r["dx"].cpu(), r["dw"].cpu()
+
+
+def save_gradients(path):
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    torch.save((*gradients(word), int(word)), path)
+
+
+def test_gradients_report_a_wait_that_ran_out(tmp_path):
+    """The hooks of the library make CTA 0 of either product leave out a stage: the status word says so, its tiles are
+    NaN and all others right."""
+    dx, dw, status = child("save_gradients", str(tmp_path / "g.pt"), SPFUSE_TEST_WAIT_NS="2000000",
+                           SPFUSE_TEST_DROP_STAGE="1")
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = gradients(word)
+    assert int(word) == 0 and not any(bool(t.isnan().any()) for t in want)
+    assert status == 0x4
+    for got, right in zip((dx, dw), want):
+        bad = got.isnan()
+        assert bool(bad.any()) and not bool(bad.all()) and torch.equal(got[~bad], right[~bad])
+
+
+def test_gradients_refuse_a_status_word_elsewhere():
+    x, sx, _ = operand(20, 30, 1)
+    wt, swt, _ = operand(30, 40, 2)
+    dy = torch.ones(20, 40, device=DEV)
+    with pytest.raises(ValueError, match="one device"):
+        ops.linear_q8_backward(dy, x, sx, wt, swt, status=torch.zeros(1, dtype=torch.int32))
+    side = torch.cuda.Stream()
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    r = ops.linear_q8_backward(dy, x, sx, wt, swt, stream=side, status=word)
+    side.synchronize()
+    assert int(word) == 0 and bool(torch.isfinite(r["dw"]).all())
