@@ -196,6 +196,9 @@ __global__ void __launch_bounds__(threads(SWAP), SWAP ? 2 : 1)
     mbar_init(&sh.drain, 1);
     fence_mbar_init();
   }
+  // An allocation waits while the SM's columns are taken, and a cluster's CTAs
+  // then wait for each other.  That ends: those of two clusters that fit on an SM
+  // together (by shared memory) want at most its 512 columns between them.
   if (warp == 1) tmem_alloc<CG>(&sh.tmem, p.tmem_cols);
   tmem_fence_before();
   if (CG == 2 || p.ks > 1)

@@ -122,6 +122,55 @@ def test_kernels_in_a_row_behind_pairs():
         assert all(torch.equal(bits(q[k]), bits(quant[k])) for k in quant)
 
 
+# ---- swapped operands, several tiles per CTA ------------------------------------------------
+
+# M, N, K, C's type, columns behind C's rows, columns per tile (256: the accumulators overlap), tiles of the busiest CTA
+BF16, F32 = torch.bfloat16, torch.float32
+SWAPPED = [(1, 50000, 4096, BF16, 0, 16, 2), (1, 50000, 4096, F32, 0, 16, 2), (18, 41193, 129, BF16, 0, 32, 2),
+           (1300, 2600, 200, BF16, 1, 48, 2), (65, 30866, 4743, F32, 0, 80, 2), (138, 34730, 2608, F32, 1, 144, 2),
+           (1679, 8260, 5243, F32, 1, 240, 3), (2770, 3330, 6545, BF16, 0, 256, 2), (15043, 624, 4714, F32, 1, 256, 2)]
+
+
+def swapped(M, N, K, dtype, pad):
+    """A product and what it is exactly; C has `pad` columns more, left alone."""
+    (a, sa, av), (b, sb, bv) = operand(M, K, M), operand(N, K, N)
+    c = torch.full((M, N + pad), 7.5, device=DEV, dtype=dtype)
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ops.matmul_q8(a, sa, b, sb, out=c[:, :N], status=word)
+    return c, int(word), (a, sa, b, sb), (av @ bv.t()).float()   # |sum| <= 36 K < 2^24
+
+
+@pytest.mark.parametrize("M,N,K,dtype,pad,bn,turns", SWAPPED)
+def test_swapped_products_of_several_tiles(M, N, K, dtype, pad, bn, turns):
+    p = plan_of(M, N, K, dtype, N + pad)
+    assert p["swapped"] and p["split_k"] == 1 and p["bn"] == bn and -(-p["tiles"] // p["ctas"]) == turns, p
+    c, word, args, want = swapped(M, N, K, dtype, pad)
+    assert word == 0 and torch.equal(c[:, :N], want.to(dtype)) and bool((c[:, N:] == 7.5).all())
+    if dtype == F32:
+        ops.matmul_q8(*args, out=c[:, :N], accumulate=True)
+        assert torch.equal(c[:, :N], 2 * want) and bool((c[:, N:] == 7.5).all())
+    for _ in range(5):   # on real values, whose sums depend on the order: the same bits every time
+        outs = [ops.matmul_q8(args[0], args[1], args[2].view(torch.float8_e5m2), args[3], out_dtype=F32) for _ in range(2)]
+        assert torch.equal(bits(outs[0]), bits(outs[1]))
+
+
+LATE = [SWAPPED[0], SWAPPED[3], SWAPPED[7]]   # two CTAs on an SM, with an unaligned C, overlapping accumulators
+
+
+def save_swapped(path):
+    torch.save([(c.cpu(), word) for c, word, _, _ in (swapped(*s[:5]) for s in LATE)], path)
+
+
+def test_swapped_products_whose_wait_runs_out(tmp_path):
+    """CTA 0 leaves out a stage: its tiles are NaN from there on, all others right, and the status word says so."""
+    late = child("save_swapped", str(tmp_path / "s.pt"), SPFUSE_TEST_WAIT_NS="2000000", SPFUSE_TEST_DROP_STAGE="1")
+    for (M, N, K, dtype, pad, _, _), (c, word) in zip(LATE, late):
+        want = swapped(M, N, K, dtype, pad)[3].to(dtype).cpu()
+        c, bad = c[:, :N], c[:, :N].isnan()
+        assert word == 0x4 and bool(bad.any()) and not bool(bad.all())
+        assert torch.equal(c[~bad], want[~bad])
+
+
 # ---- the status word of the gradients ------------------------------------------------------
 
 def gradients(word):
