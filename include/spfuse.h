@@ -175,12 +175,16 @@ sp_status_t sp_rs_dropout_residual_norm_fwd_rows(const sp_rs_desc_t* desc,
  * quantised in 128 x 128 blocks, one row per 128 rows.  Values and scales
  * have row strides in bytes that are multiples of 16 and 16-byte aligned
  * bases (multiples of 128 bytes are faster: no row then straddles cache
- * lines); what lies between the end of a row and its stride is neither read
- * as a value nor written.
+ * lines); what lies between the end of a row and its stride is neither used
+ * as a value nor written.  sp_matmul_q8 reads scale bytes in aligned pieces of
+ * 16: the pieces that hold a row's scales have to be readable as a whole, the
+ * last row's (or a single row's) too.
  * Quantising a group: s is the smallest integer with max|x| <= 448 * 2^s
  * (e4m3) or 57344 * 2^s (e5m2), at least -127; byte = s + 127 and
  * q = x * 2^-s rounded to nearest even.  A group of zeros has s = 0.  A group
- * that holds an infinity or a NaN gets byte 255 and NaN values. */
+ * that holds an infinity or a NaN gets byte 255 and NaN values.  Values are
+ * taken as fp32: one of an 8-bit x that fp32 does not hold (448 * 2^120, say,
+ * with scale byte 247) counts as an infinity. */
 
 /* The forward of the SP region with the norm's output in 8 bits, for a
  * column-parallel product in 8 bits behind it (and a half as large
