@@ -279,7 +279,7 @@ typedef struct sp_matmul_q8_desc_t {
 } sp_matmul_q8_desc_t;
 
 /* c: element-aligned, must not overlap A, B or the scales; only its M x N
- * elements are written.  K == 0 writes zeros (or leaves C when accumulating);
+ * elements are written.  K == 0 writes zeros (when accumulating it leaves C);
  * A, B and the scales may then be NULL.  M == 0 or N == 0 returns SP_OK at
  * once.  Errors: SP_ERR_DTYPE (types; accumulating in bf16), SP_ERR_SHAPE
  * (sizes, strides), SP_ERR_INVALID_ARG (NULL pointers, scale_rows,
@@ -484,7 +484,8 @@ typedef struct sp_matmul_q8_plan_t {
 
 /* What sp_matmul_q8 would launch for `desc` on a device with `sms`
  * multiprocessors and `smem_optin` bytes of opt-in shared memory per block,
- * with C 16-byte aligned; all zero where M or N is 0 and nothing is launched.
+ * with C 16-byte aligned; all zero where M or N is 0, or K is 0 when
+ * accumulating, and nothing is launched.
  * Host arithmetic only.  Errors: the descriptor's, SP_ERR_INVALID_ARG for a
  * NULL `out`, non-positive limits or too little shared memory for the tile. */
 sp_status_t sp_matmul_q8_plan(const sp_matmul_q8_desc_t* desc, int32_t sms, int32_t smem_optin,

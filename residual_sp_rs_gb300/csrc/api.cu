@@ -574,6 +574,7 @@ sp_status_t sp_matmul_q8(const sp_matmul_q8_desc_t* d, const uint8_t* a, const u
   if (!aligned(a, 16) || !aligned(a_scale, 16) || !aligned(b, 16) || !aligned(b_scale, 16) ||
       !aligned(c, d->c_dtype == SP_ELEM_F32 ? 4 : 2))
     return SP_ERR_ALIGN;
+  if (d->K == 0 && d->accumulate) return SP_OK;  // C stays, the signs of its zeros too
   MatmulArgs m = matmul_args(*d);
   m.a = a;
   m.a_scale = a_scale;
@@ -717,7 +718,7 @@ sp_status_t sp_matmul_q8_plan(const sp_matmul_q8_desc_t* desc, int32_t sms, int3
   if (st != SP_OK) return st;
   if (!out || sms < 1 || smem_optin < 1) return SP_ERR_INVALID_ARG;
   std::memset(out, 0, sizeof(*out));
-  if (desc->M == 0 || desc->N == 0) return SP_OK;  // nothing is launched
+  if (desc->M == 0 || desc->N == 0 || (desc->K == 0 && desc->accumulate)) return SP_OK;  // nothing is launched
   describe_matmul_q8(matmul_args(*desc), sms, smem_optin, out);
   // a ring of two stages and, with K split, the fp32 sums in the ring's place
   if (out->stages < 2 || (out->split_k > 1 && out->stages * out->stage_bytes < (int64_t)out->bn * 512)) {

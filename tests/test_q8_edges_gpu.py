@@ -171,6 +171,15 @@ def test_swapped_products_whose_wait_runs_out(tmp_path):
         assert torch.equal(c[~bad], want[~bad])
 
 
+def test_adding_an_empty_sum_keeps_the_signs_of_zeros():
+    a, sa = ops.q8_empty(5, 0, DEV, torch.float8_e4m3fn), ops.q8_empty(5, 0, DEV)
+    c = torch.full((5, 5), -0.0, device=DEV)
+    ops.matmul_q8(a, sa, a, sa, out=c, accumulate=True)
+    assert bool(torch.signbit(c).all())
+    ops.matmul_q8(a, sa, a, sa, out=c)
+    assert not bool(torch.signbit(c).any()) and bool((c == 0).all())
+
+
 # ---- the status word of the gradients ------------------------------------------------------
 
 def gradients(word):

@@ -1,4 +1,6 @@
 """Host-side checks of the 8-bit operators' launches (no GPU)."""
+import ctypes
+
 import pytest
 
 
@@ -49,3 +51,15 @@ def test_clusters_never_wait_for_tensor_memory(spf):
         return max([0] + [cols + most(room - size) for cols, size in least.items() if size <= room])
 
     assert most(sm) <= 512, least
+
+
+def test_adding_an_empty_sum_launches_nothing(spf):
+    """C += A B^T with K = 0 leaves C, bit for bit: there is nothing to launch, and no device is needed."""
+    fake = 1 << 20
+    d = spf.SpMatmulQ8Desc(5, 7, 0, 16, 16, 16, 16, 7, 2, 2, 0, 1, 1, 1, None)
+    assert spf.lib().sp_matmul_q8(ctypes.byref(d), None, None, None, None, fake, None) == 0
+    assert spf.lib().sp_matmul_q8(ctypes.byref(d), None, None, None, None, None, None) == 1   # its checks stay
+    assert spf.lib().sp_matmul_q8(ctypes.byref(d), None, None, None, None, fake + 2, None) == 3
+    assert spf.sp_matmul_q8_plan(d, 152, 232448)["ctas"] == 0
+    d.accumulate = 0
+    assert spf.sp_matmul_q8_plan(d, 152, 232448)["ctas"] > 0
