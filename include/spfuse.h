@@ -191,9 +191,10 @@ sp_status_t sp_rs_dropout_residual_norm_fwd_rows(const sp_rs_desc_t* desc,
  * all-gather in front of that): sp_rs_dropout_residual_norm_fwd with y
  * quantised to e4m3, one scale per token and 128 columns, straight from its
  * fp32 value.  With T = 1 and p = 0 it is the residual's addition and the norm.
- * A bf16 h is the sum's fp32 value rounded to bf16, so it can differ from
- * that call's by one step where the exact sum lies within half an fp32 step
- * of a bf16 midpoint; the norm is of the stored h either way.  mask_out is
+ * A bf16 h is the sum to one fp32 step, rounded to bf16: at most 1/2 + 2^-16
+ * steps off.  It differs from that call's, by one step, only where the exact
+ * sum lies within an fp32 step of a bf16 midpoint (0.9% of the elements at
+ * p = 0.1, hardly any at p = 0 or 1/2); the norm is of the stored h either way.  mask_out is
  * the same and sp_rs_dropout_residual_norm_bwd is its backward too (y's
  * rounding is passed straight through, as that of a 16-bit y is).
  *

@@ -78,6 +78,33 @@ def test_requantisation_goes_on_without_its_copies(tmp_path, stage):
             assert want[name] is None or torch.equal(got[name], want[name]), (M, K, name)
 
 
+# ---- the residual stream of the 8-bit forward ------------------------------------------------
+
+@pytest.mark.parametrize("H", [768, 16384])
+@pytest.mark.parametrize("p", [0.0, 0.1, 0.5])
+def test_residual_far_below_the_partials(H, p):
+    """h is the sum to one fp32 step, which is 2^-16 bf16 steps, rounded to bf16 (half a step), also where the residual
+    is 2^-12 to 2^-30 of the partials or they of it; it is the other forward's h unless the sum is that near a midpoint
+    of bf16 values."""
+    rows = 64
+    g = torch.Generator(device=DEV).manual_seed(H)
+    part = torch.randn(rows, 1, H, generator=g, device=DEV)
+    far = torch.tensor([0, 8, 12, 13, 16, 17, 20, 24, 30, -8, -12, -13, -16, -20, -30, 40], device=DEV).repeat(rows // 16)
+    res = torch.randn(rows, H, generator=g, device=DEV) * torch.ldexp(torch.ones(rows, device=DEV), -far)[:, None]
+    part[0, 0, :8], res[0, :8] = 1.0, -1.0   # and where they cancel
+    part, res, gamma = part.bfloat16(), res.bfloat16(), torch.ones(H, device=DEV).bfloat16()
+    d = ops.make_desc(1, 0, rows, 1, H, "bf16", "rms", p, 1e-6, 7, 1)
+    f, ref = ops.forward_q8(d, [part], res, gamma), ops.forward(d, [part], res, gamma)
+    keep = 1.0 if p == 0 else f["mask"].double()
+    exact = res.double() + part.view(rows, H).double() * keep / (1.0 - float(d.p))   # 2^-52 off
+    step = torch.ldexp(torch.ones_like(exact), (torch.frexp(exact)[1] - 8).clamp_min(-133))   # between bf16 values
+    h, other = f["h"].double(), ref["h"].double()
+    assert bool(((h - exact).abs() <= (0.5 + 2.0 ** -16 * (1 + 2.0 ** -6)) * step).all())
+    moved = h != other
+    assert bool((((h + other) / 2 - exact).abs()[moved] <= 2.0 ** -16 * (1 + 2.0 ** -6) * step[moved]).all())
+    assert p == 0.1 or not bool(moved.any())
+
+
 # ---- products in a row ----------------------------------------------------------------------
 
 def plan_of(M, N, K, out_dtype=torch.float32, ldc=None):
