@@ -207,6 +207,73 @@ def test_adding_an_empty_sum_keeps_the_signs_of_zeros():
     assert not bool(torch.signbit(c).any()) and bool((c == 0).all())
 
 
+# ---- values and scales at the ends, offsets past 32 bits ------------------------------------
+
+@pytest.mark.parametrize("M,N", [(5, 40), (300, 300)])
+def test_smallest_scale_and_infinities(M, N):
+    """Scale byte 0 is 2^-127, and an infinity (e5m2) is one in its row and its sign, NaN against zeros."""
+    (a, sa, av), (b, sb, bv) = operand(M, 300, 1), operand(N, 300, 2)
+    sa[:, 1], sb[:, 1] = 0, 254   # 2^-127 2^127
+    av, bv = av.clone(), bv.clone()
+    av[:, 128:256], bv[:, 128:256] = a[:, 128:256].double(), b[:, 128:256].double()
+    assert torch.equal(ops.matmul_q8(a, sa, b, sb, out_dtype=F32).double(), av @ bv.t())
+    q = a.float().to(torch.float8_e5m2)   # -3..3 are e5m2 values
+    x = ops.q8_empty(M, 300, DEV, torch.float8_e5m2)
+    x.copy_(q)
+    x.view(torch.uint8)[3, 7] = 0x7C      # infinity
+    want = (av @ bv.t()).float()
+    want[3] = torch.where(bv[:, 7] == 0, torch.nan, torch.sign(bv[:, 7]) * torch.inf).float()
+    got = ops.matmul_q8(x, sa, b, sb, out_dtype=F32)
+    assert bool(((got == want) | (got.isnan() & want.isnan())).all())
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 bytes and 2^31 elements: the last rows and columns are what a call on them alone gives."""
+    M, K = 131200 + 77, 32768 + 128
+    x = torch.empty(M, K, device=DEV, dtype=BF16)
+    for i in range(0, M, 32768):
+        x[i:i + 32768].normal_()
+    r = ops.quantize_q8(x, colwise=True)
+    tail = x[131072:]                     # a multiple of 128 rows down
+    t = ops.quantize_q8(tail, colwise=True)
+    assert torch.equal(bits(r["q"][131072:]), bits(t["q"])) and torch.equal(r["scale"][131072:], t["scale"])
+    assert torch.equal(bits(r["qt"][:, 131072:]), bits(t["qt"])) and torch.equal(r["scale_t"][:, 1024:], t["scale_t"])
+    del x, tail, r, t
+    x, s = ops.q8_empty(M, K, DEV), ops.q8_empty(M, -(-K // 128), DEV)
+    for i in range(0, M, 16384):
+        q, e, v = operand(min(16384, M - i), K, i)
+        x[i:i + 16384], s[i:i + 16384] = q.view(torch.uint8), e
+    x, v = x.view(torch.float8_e4m3fn), v[-1000:].clone()   # the last rows' values
+    del q, e
+    z = ops.quantize_q8(x, scale=s, rowwise=False, colwise=True)
+    u = ops.quantize_q8(x[131072:], scale=s[131072:], rowwise=False, colwise=True)
+    assert torch.equal(bits(z["qt"][:, 131072:]), bits(u["qt"])) and torch.equal(z["scale_t"][:, 1024:], u["scale_t"])
+    del z, u
+    # x as A and as B, with few and with many rows of the other operand; |sum| <= 36 K < 2^24
+    w, sw, wv = operand(300, K, 5)
+    for rows in (3, 300):
+        c = ops.matmul_q8(x, s, w[:rows], sw[:rows], out_dtype=F32)
+        assert torch.equal(c[-len(v):], (v @ wv[:rows].t()).float())
+        c = ops.matmul_q8(w[:rows], sw[:rows], x, s, out_dtype=F32)
+        assert torch.equal(c[:, -len(v):], (wv[:rows] @ v.t()).float())
+    del x, s
+    # C past 32 bits, of sums that fp32 and bf16 hold
+    (a, sa, av), (b, sb, bv) = operand(66000, 16, 1), operand(33000, 16, 2)
+    c = ops.matmul_q8(a, sa, b, sb, out_dtype=F32)
+    assert torch.equal(c[-500:], (av[-500:] @ bv.t()).float()) and torch.equal(c[:, -500:], (av @ bv[-500:].t()).float())
+
+
+def test_forward_past_32_bits():
+    rows, H = 263000, 8192
+    part = torch.empty(rows, 1, H, device=DEV, dtype=BF16).normal_()
+    res = torch.empty(rows, H, device=DEV, dtype=BF16).normal_()
+    gamma = torch.ones(H, device=DEV, dtype=BF16)
+    f = ops.forward_q8(ops.make_desc(1, 0, rows, 1, H, "bf16", "rms", 0.0, 1e-6, 7, 1), [part], res, gamma)
+    t = ops.forward_q8(ops.make_desc(1, 0, 1000, 1, H, "bf16", "rms", 0.0, 1e-6, 7, 1), [part[-1000:]], res[-1000:], gamma)
+    assert torch.equal(f["h"][-1000:], t["h"]) and torch.equal(f["rstd"][-1000:], t["rstd"])
+    assert torch.equal(bits(f["q"][-1000:]), bits(t["q"])) and torch.equal(f["scale"][-1000:], t["scale"])
+
+
 # ---- the status word of the gradients ------------------------------------------------------
 
 def gradients(word):
