@@ -28,7 +28,7 @@
 // group is 16 neighbouring lanes' vectors (its maximum is four shuffles); the
 // fp32 value of y is scaled and rounded to 8 bits at once, without the
 // rounding to bf16 in between.  h is rounded through fp32 (residual_vec8_via_f32).
-// T=2, 4096 x 768, p=0.1: 8.8 us against 7.6 with y in bf16 (6 more ALU
+// T=2, 4096 x 768, p=0.1: 8.4 us against 7.8 with y in bf16 (6 more ALU
 // instructions an element for 3.1 MB less); T=8, 4096 x 4096 LayerNorm: 59 us
 // against 61, both at the copy bandwidth of their bytes (92%).
 //

@@ -22,9 +22,11 @@
 // from there on, so that only time is lost.
 //
 // 66 M values: bf16 along the rows 32.5 us (90% of the copy bandwidth), along
-// the columns 36 (81%), both 47 (82%); 8-bit along the rows 29 us (67%), along
-// the columns 35 (56%: 13 instructions a value and four barriers a tile);
-// 33.5 M fp32 values in blocks, both ways, 35 us (84%).
+// the columns 35 (83%), both 47 (82%); 8-bit along the rows 29 us (67%), along
+// the columns 35 (55%); 33.5 M fp32 values in blocks, both ways, 35 us (85%).
+// The 8-bit columns fill no pipe (issue 56%, shared memory 48%): 13 instructions
+// a value between four barriers a tile, whose warps stall at the barriers, on
+// shared memory and on their own last instruction in equal parts.
 #include "common.cuh"
 #include "launch.h"
 #include "q8.cuh"
