@@ -105,6 +105,46 @@ def test_residual_far_below_the_partials(H, p):
     assert p == 0.1 or not bool(moved.any())
 
 
+LATE_NORMS = [(768, "rms"), (4096, "ln"), (8192, "ln")]   # rows in stages of several, of one, and (T = 8) in column chunks
+
+
+def norms(status):
+    """The 8-bit forward of 1600 and more rows: its outputs, what the status word says, and the rows of CTA 0."""
+    out = []
+    for H, norm in LATE_NORMS:
+        T = 8 if H == 8192 else 2
+        g = torch.Generator(device=DEV).manual_seed(H)
+        rand = lambda *shape: torch.randn(shape, generator=g, device=DEV).bfloat16()
+        status.zero_()
+        d = ops.make_desc(T, 0, 1600, 1, H, "bf16", norm, 0.1, 1e-6, 7, T, status=status)
+        f = ops.forward_q8(d, [rand(1600, 1, H) for _ in range(T)], rand(1600, H), rand(H), rand(H) if norm == "ln" else None)
+        torch.cuda.synchronize()
+        out.append(({k: bits(v) for k, v in f.items() if v is not None}, f["rstd"].cpu(), int(status)))
+    return out
+
+
+def save_norms(path):
+    torch.save(norms(torch.zeros(1, dtype=torch.int32, device=DEV)), path)
+
+
+def test_forward_whose_wait_runs_out(tmp_path):
+    """CTA 0 leaves out a stage: rows of its that it did not finish have NaN in rstd, all other rows are right, and the
+    status word says so."""
+    late = child("save_norms", str(tmp_path / "n.pt"), SPFUSE_TEST_WAIT_NS="2000000", SPFUSE_TEST_DROP_STAGE="1")
+    props = torch.cuda.get_device_properties(0)
+    for (H, norm), (got, rstd, word), (want, _, clean) in zip(LATE_NORMS, late, norms(torch.zeros(1, dtype=torch.int32, device=DEV))):
+        d = ops.make_desc(8 if H == 8192 else 2, 0, 1600, 1, H, "bf16", norm, 0.1, 1e-6, 7, 8 if H == 8192 else 2)
+        plan = ops.sp_plan_describe(d, props.multi_processor_count, getattr(props, "shared_memory_per_block_optin", 232448))["fwd"]
+        assert plan["tma"] and (word, clean) == (0x1, 0)
+        bad = rstd.isnan()
+        # (in column chunks stage 1 is part of row 0, and a single row group stops there, before all the other rows)
+        assert bool(bad.any()) and not bool(bad[plan["rows_per_cta"]:].any())
+        assert plan["chunked"] or not bool(bad[:plan["rows_per_cta"]].all())
+        for k in want:
+            if k != "mean":   # of the unfinished rows it is not written either
+                assert torch.equal(got[k].view(len(rstd), -1)[~bad], want[k].view(len(rstd), -1)[~bad]), (H, k)
+
+
 # ---- products in a row ----------------------------------------------------------------------
 
 def plan_of(M, N, K, out_dtype=torch.float32, ldc=None):
